@@ -1,0 +1,224 @@
+"""w4a16_moe_route and w4a16_moe_combine on the GPU against 64-bit definitions
+(moe_ref): choices, offsets and lists equal, weights within two roundings of
+fp32 (the 64-bit score chain adds far less), sums within their bound."""
+import math
+import sys
+
+import numpy as np
+import pytest
+
+import moe_ref
+
+pytestmark = pytest.mark.gpu
+SENTINEL = -77
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible to torch")
+    import w4a16_weight_only_gemm_amd  # noqa: F401  (fails loudly if the library is missing)
+    yield
+
+
+def log(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+def run_route(logits, bias, top_k, bf16=False, **kw):
+    """One call; `logits` fp32 values (already bf16-representable with bf16)."""
+    import torch
+
+    import w4a16_weight_only_gemm_amd as w4
+    T, E = logits.shape
+    dl = torch.from_numpy(np.ascontiguousarray(logits, np.float32)).cuda()
+    if bf16:
+        dl = dl.to(torch.bfloat16)
+    db = None if bias is None else torch.from_numpy(np.asarray(bias, np.float32)).cuda()
+    ids = torch.full((T, top_k), SENTINEL, dtype=torch.int32, device="cuda")
+    w = torch.full((T, top_k), float("nan"), device="cuda")
+    off = torch.full((E + 1,), SENTINEL, dtype=torch.int32, device="cuda")
+    rows = torch.full((T * top_k,), SENTINEL, dtype=torch.int32, device="cuda")
+    n = w4.w4a16_moe_route_workspace_bytes(T, E)
+    ws = torch.full((max(n // 4, 1),), SENTINEL, dtype=torch.int32, device="cuda")
+    kw = dict(kw)
+    kw["scoring"] = (w4.W4A16_ROUTE_SIGMOID if kw.get("scoring") == "sigmoid"
+                     else w4.W4A16_ROUTE_SOFTMAX)
+    w4.w4a16_moe_route(dl, db, T, E, top_k, ids, w, off, rows, ws, **kw)
+    torch.cuda.synchronize()
+    return ids.cpu().numpy(), w.cpu().numpy(), off.cpu().numpy(), rows.cpu().numpy()
+
+
+def check_route(logits, bias, top_k, bf16=False, **kw):
+    if bf16:
+        logits = moe_ref.bf16_value(moe_ref.bf16_bits(logits)).astype(np.float32)
+    log("route", logits.shape, top_k, kw)
+    got = run_route(logits, bias, top_k, bf16, **kw)
+    ref = moe_ref.route(logits, None if bias is None else np.float32(bias), top_k, **kw)
+    assert np.array_equal(got[0], ref[0])
+    assert np.array_equal(got[2], ref[2])
+    assert np.array_equal(got[3], ref[3])
+    assert np.all(np.abs(got[1] - ref[1]) <= 2 * moe_ref.F32 * np.abs(ref[1]) + 1e-45)
+
+
+@pytest.mark.parametrize("E,top_k", [(1, 1), (3, 2), (8, 2), (60, 4), (64, 6), (65, 8), (128, 8),
+                                     (257, 8), (384, 8), (512, 32), (1000, 10), (1024, 32)])
+@pytest.mark.parametrize("T", [1, 5])
+def test_experts_and_top_k(T, E, top_k):
+    rng = np.random.default_rng(E * 100 + T)
+    z = rng.standard_normal((T, E)).astype(np.float32) * 2
+    check_route(z, None, top_k)
+    check_route(z, rng.standard_normal(E) * 0.1, top_k, scoring="sigmoid", renormalize=False,
+                scale=2.5, bf16=True)
+
+
+@pytest.mark.parametrize("T", [16, 17, 32, 33, 64, 100, 1000])
+def test_tokens(T):
+    rng = np.random.default_rng(T)
+    z = rng.standard_normal((T, 40)).astype(np.float32)
+    check_route(z, None, 3)
+    check_route(z, rng.standard_normal(40) * 0.1, 3, scoring="sigmoid", groups=4, groups_kept=2,
+                group_top=2)
+
+
+def test_more_chunks_than_one_pass_sums():
+    rng = np.random.default_rng(3)
+    T = 32 * 256 + 33  # one chunk of 32 tokens past 256, and a ragged one
+    check_route(rng.standard_normal((T, 20)).astype(np.float32), None, 2)
+    check_route(rng.standard_normal((T - 33, 20)).astype(np.float32), None, 2)
+
+
+@pytest.mark.parametrize("groups,kept,E", [(2, 1, 6), (8, 4, 256), (3, 2, 39), (64, 5, 64),
+                                           (33, 7, 66), (4, 4, 128), (5, 1, 1020)])
+@pytest.mark.parametrize("scoring,group_top,bias", [("softmax", 1, False), ("sigmoid", 2, True),
+                                                    ("softmax", 2, True)])
+def test_groups(groups, kept, E, scoring, group_top, bias):
+    rng = np.random.default_rng(groups * 10 + kept)
+    z = rng.standard_normal((9, E)).astype(np.float32) * 1.5
+    b = rng.standard_normal(E) * 0.05 if bias else None
+    check_route(z, b, min(8, E // groups * kept), scoring=scoring, groups=groups,
+                groups_kept=kept, group_top=group_top)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_equal_values_go_to_the_lowest_index(scoring, bias):
+    rng = np.random.default_rng(8)
+    z = rng.integers(-2, 3, (40, 200)).astype(np.float32)  # five values over 200 experts
+    z[0] = 0.0
+    z[1] = np.where(rng.random(200) < 0.5, 0.0, -0.0)
+    check_route(z, np.zeros(200) if bias else None, 8, scoring=scoring)
+    check_route(z, np.zeros(200) if bias else None, 8, scoring=scoring, groups=8, groups_kept=3)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("T", [12, 50])
+def test_masked_and_extreme_logits(scoring, bias, renormalize, T):
+    """-inf and NaN are never chosen, rows that leave nothing go nowhere, +inf and
+    the type's extremes are ordinary large values."""
+    rng = np.random.default_rng(5)
+    E = 70
+    low = float(np.finfo(np.float32).min)
+    z = rng.standard_normal((T, E)).astype(np.float32)
+    z[0] = -np.inf
+    z[1] = np.nan
+    z[2, 3:] = -np.inf
+    z[3, ::2] = np.nan
+    z[4] = low
+    z[5, 10:] = low
+    z[6, 7] = np.inf
+    z[7] = -low
+    z[8, 68:] = -np.inf
+    z[9] = -np.inf
+    z[9, 69] = low
+    b = rng.standard_normal(E) * 0.1 if bias else None
+    kw = dict(scoring=scoring, renormalize=renormalize)
+    check_route(z, b, 5, **kw)
+    check_route(z, b, 5, groups=7, groups_kept=2, group_top=2, **kw)
+
+
+def test_every_token_to_one_expert():
+    z = np.zeros((300, 128), np.float32)
+    z[:, 77] = 5.0
+    check_route(z, None, 1)
+
+
+def test_no_tokens():
+    import torch
+
+    import w4a16_weight_only_gemm_amd as w4
+    off = torch.full((9,), SENTINEL, dtype=torch.int32, device="cuda")
+    e = torch.empty(0, dtype=torch.int32, device="cuda")
+    f = torch.empty(0, device="cuda")
+    w4.w4a16_moe_route(torch.empty(0, 8, device="cuda"), None, 0, 8, 2, e, f, off, e, None)
+    torch.cuda.synchronize()
+    assert off.tolist() == [0] * 9
+
+
+def test_repeated_calls_give_the_same_bits():
+    z = np.random.default_rng(1).standard_normal((500, 96)).astype(np.float32)
+    first = run_route(z, np.linspace(-.1, .1, 96), 6, scoring="sigmoid")
+    for _ in range(3):
+        again = run_route(z, np.linspace(-.1, .1, 96), 6, scoring="sigmoid")
+        assert all(np.array_equal(a, b) for a, b in zip(first, again))
+
+
+# ------------------------------------------------------------------ combine
+
+@pytest.mark.parametrize("T,k,N", [(1, 1, 1), (1, 8, 5120), (3, 2, 7), (33, 4, 264), (5, 32, 100),
+                                   (7, 3, 2049), (257, 8, 512)])
+@pytest.mark.parametrize("base", [False, True])
+def test_combine(T, k, N, base):
+    import torch
+
+    import w4a16_weight_only_gemm_amd as w4
+    log("combine", T, k, N, base)
+    rng = np.random.default_rng(T * N + k)
+    yb = moe_ref.bf16_bits(rng.standard_normal((T * k, N)).astype(np.float32))
+    bb = moe_ref.bf16_bits(rng.standard_normal((T, N)).astype(np.float32))
+    ids = rng.integers(-1, 5, (T, k)).astype(np.int32)  # about a sixth left out
+    w = rng.random((T, k)).astype(np.float32)
+    yb.reshape(T, k, N)[ids < 0] = 0x7FC0               # rows left out are not read
+    ref, tol = moe_ref.combine(moe_ref.bf16_value(yb), ids, w.astype(np.float64),
+                               moe_ref.bf16_value(bb) if base else None)
+    dev = lambda a: torch.from_numpy(a.view(np.int16)).cuda().view(torch.bfloat16)  # noqa: E731
+    y, b = dev(yb), dev(bb)
+    out = torch.full((T, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    di, dw = torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda()
+    w4.w4a16_moe_combine(y, di, dw, b if base else None, out, T, k, N)
+    torch.cuda.synchronize()
+    got = out.view(torch.int16).cpu().numpy().view(np.uint16)
+    moe_ref.check(got, ref, tol)
+    if base:  # in place
+        w4.w4a16_moe_combine(y, di, dw, b, b, T, k, N)
+        torch.cuda.synchronize()
+        assert np.array_equal(b.view(torch.int16).cpu().numpy().view(np.uint16), got)
+
+
+def test_binding_refuses_wrong_tensors():
+    import torch
+
+    import w4a16_weight_only_gemm_amd as w4
+    z = torch.zeros(4, 16, device="cuda")
+    i = torch.zeros(8, dtype=torch.int32, device="cuda")
+    f = torch.zeros(8, device="cuda")
+    off = torch.zeros(17, dtype=torch.int32, device="cuda")
+    good = dict(logits=z, bias=None, ids=i, weights=f, offsets=off, rows=i.clone())
+
+    def call(**kw):
+        d = {**good, **kw}
+        w4.w4a16_moe_route(d["logits"], d["bias"], 4, 16, 2, d["ids"], d["weights"], d["offsets"],
+                           d["rows"], None)
+    call()
+    for kw in (dict(logits=z.half()), dict(ids=f), dict(weights=i), dict(offsets=off.long()),
+               dict(bias=z.half()[0])):
+        with pytest.raises(TypeError):
+            call(**kw)
+    for kw in (dict(logits=z[:3]), dict(ids=i[:7]), dict(offsets=off[:16]), dict(rows=i[:7]),
+               dict(logits=torch.zeros(16, 4, device="cuda").t()), dict(weights=f.cpu())):
+        with pytest.raises(ValueError):
+            call(**kw)
+    assert math.isfinite(float(f.sum()))

@@ -463,3 +463,6 @@ def w4a16_read_probe(buf, nbytes: int, sink, sink_bytes: int = READ_PROBE_SINK_B
     rc = read_probe_status(buf, nbytes, sink, sink_bytes, stream)
     if rc != W4A16_OK:
         raise W4A16Error(rc, "w4a16_read_probe")
+
+
+from ._moe import *  # noqa: E402,F401,F403  (the operators of include/w4a16_moe.h)

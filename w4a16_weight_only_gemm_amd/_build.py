@@ -9,7 +9,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libw4a16.so")
 SOURCES = ["w4a16_host.cpp", "w4a16_plain.hip", "w4a16_skinny.hip", "w4a16_large.hip", "w4a8.hip",
-           "w4a16_probe.hip", "w4a16_noalloc.hip"]
+           "w4a16_probe.hip", "w4a16_noalloc.hip", "w4a16_moe_host.cpp", "w4a16_moe.hip",
+           "w4a16_experts.hip", "w8a8.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 
