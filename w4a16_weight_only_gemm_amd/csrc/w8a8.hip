@@ -11,9 +11,9 @@
 //    as contiguous 1 KB tiles, one per wave and 64-deep step, each read from
 //    HBM once. Bound by HBM.
 //  * w8a8_tile_kernel (many rows): a workgroup owns a row x column tile; its
-//    waves form WM x WN and each an MB x NB grid of 16 x 16 blocks.
-//    Activations are staged through LDS (double-buffered, XOR-swizzled), the
-//    weight tiles go straight into registers. Bound by MFMA.
+//    waves form WM x WN and each an MB x NB grid of 16 x 16 blocks. Both
+//    operands are copied to LDS (double-buffered). Bound by the rate of those
+//    copies and by MFMA.
 //
 // The last k step may be partial: its weight codes past K are zero, so the
 // activation codes there may be anything; their addresses are clamped into the
@@ -21,8 +21,10 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "w4a16_device.h"
+#include "w4a16_launch.h"
 #include "w4a16_moe_launch.h"
 
 namespace w4a16_internal {
@@ -34,68 +36,113 @@ __device__ __forceinline__ i32x4 mfma_i8(i32x4 a, i32x4 b, i32x4 c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
+// LDS slot of piece p of a 128-byte row: conflict-free for the staging writes
+// (eight rows a wave) and the fragment reads (sixteen rows, one piece).
+__device__ __forceinline__ int t8_slot(int piece, int row) {
+  return piece ^ (row & 7) ^ ((row >> 3) & 1);
+}
+
 // --------------------------------------------------------------- few rows
 
-template <int MB, int NB, int WAVES, int P>
+// A wave works through pairs of steps (128 k). XS: it loads its rows' 128-byte
+// pieces coalesced (8 lanes a row) and turns them into operands through a
+// wave-private LDS area; read in operand order, a load's 16 consecutive lanes
+// sit in 16 rows, 16 cache lines for 256 bytes.
+template <int MB, int NB, int WAVES, bool XS>
 __global__ __launch_bounds__(64 * WAVES) void w8a8_small_kernel(const W8A8Args a) {
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
   const int c16 = lane & 15, lg = lane >> 4;
-  const int S = (a.K + 63) / 64, NCB = (a.N + 15) / 16;
+  const int S = (a.K + 63) / 64, S2 = (S + 1) / 2, NCB = (a.N + 15) / 16;
   const int b0 = blockIdx.x * NB, m0 = blockIdx.y * 16 * MB;
-  const int s0 = static_cast<int>(static_cast<long long>(S) * wave / WAVES);
-  const int s1 = static_cast<int>(static_cast<long long>(S) * (wave + 1) / WAVES);
-  extern __shared__ __attribute__((aligned(16))) int q8s_red[];
+  const int s0 = static_cast<int>(static_cast<long long>(S2) * wave / WAVES);
+  const int s1 = static_cast<int>(static_cast<long long>(S2) * (wave + 1) / WAVES);
+  extern __shared__ __attribute__((aligned(16))) int q8s_lds[];  // operands, then the waves' sums
+  unsigned char* const area = reinterpret_cast<unsigned char*>(q8s_lds) + wave * (MB * 2048);
 
   gptr<const i32x4> wbase[NB];
-  gptr<const uint8_t> xrow[MB];
+  constexpr int XR = XS ? 2 * MB : MB;
+  gptr<const uint8_t> xrow[XR];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)  // past the last block: clamped, not stored
     wbase[nb] = reinterpret_cast<gptr<const i32x4>>(
                     to_global(a.qweight) + static_cast<size_t>(min(b0 + nb, NCB - 1)) * S * 1024) + lane;
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb)  // past the last row: repeats it, not stored
-    xrow[mb] = to_global(a.xq) + static_cast<size_t>(min(m0 + 16 * mb + c16, a.M - 1)) * a.K;
+  for (int i = 0; i < XR; ++i) {  // past the last row: repeats it, not stored
+    const int r = XS ? 8 * i + lane / 8 : 16 * i + c16;
+    xrow[i] = to_global(a.xq) + static_cast<size_t>(min(m0 + r, a.M - 1)) * a.K;
+  }
 
   struct Stage {
-    i32x4 w[NB], x[MB];
+    i32x4 w[2][NB], x[2][MB];
   };
   auto load = [&](Stage& st, int s) {
     s = min(s, s1 - 1);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) st.w[nb] = __builtin_nontemporal_load(wbase[nb] + static_cast<size_t>(s) * 64);
-    const int k = min(64 * s + 16 * lg, a.K - 16);
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) st.x[mb] = *reinterpret_cast<gptr<const i32x4>>(xrow[mb] + k);
+      for (int nb = 0; nb < NB; ++nb)  // past the last step: re-read, not used
+        st.w[h][nb] = __builtin_nontemporal_load(wbase[nb] + static_cast<size_t>(min(2 * s + h, S - 1)) * 64);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        const int k = min(128 * s + (XS ? 16 * (lane & 7) : 64 * h + 16 * lg), a.K - 16);
+        st.x[h][mb] = *reinterpret_cast<gptr<const i32x4>>(xrow[XS ? 2 * mb + h : mb] + k);
+      }
   };
   i32x4 acc[MB][NB];
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = i32x4{0, 0, 0, 0};
-  if (s1 > s0) {
-    Stage st[P];
+  auto compute = [&](const Stage& st, int c) {
+    if constexpr (XS) {  // rows 16 mb + 8 h + lane / 8, piece lane % 8
 #pragma unroll
-    for (int p = 0; p < P; ++p) load(st[p], s0 + p);
-    for (int c = s0; c < s1; c += P) {
+      for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-      for (int p = 0; p < P; ++p)
-        if (c + p < s1) {
-#pragma unroll
-          for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = mfma_i8(st[p].x[mb], st[p].w[nb], acc[mb][nb]);
-          load(st[p], c + p + P);
+        for (int h = 0; h < 2; ++h) {
+          const int row = 8 * h + lane / 8;
+          *reinterpret_cast<i32x4*>(area + (16 * mb + row) * 128 + t8_slot(lane & 7, row) * 16) = st.x[h][mb];
         }
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (2 * c + h >= S) break;  // uniform: the last pair may have one step
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        i32x4 xa = st.x[h][mb];
+        if constexpr (XS)
+          xa = *reinterpret_cast<const i32x4*>(area + (16 * mb + c16) * 128 + t8_slot(4 * h + lg, c16) * 16);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = mfma_i8(xa, st.w[h][nb], acc[mb][nb]);
+      }
+    }
+  };
+  if (s1 > s0) {
+    // the next pair's loads are issued before a pair's math, into the other of
+    // two register sets (past the last pair: re-read, not used)
+    Stage st0, st1;
+    load(st0, s0);
+    for (int c = s0; c < s1; c += 2) {
+      load(st1, c + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(st0, c);
+      if (c + 1 < s1) {
+        load(st0, c + 2);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(st1, c + 1);
+      }
+    }
   }
+  if constexpr (XS) __syncthreads();  // the operand areas are no longer read
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        q8s_red[(((wave * MB + mb) * NB + nb) * 4 + r) * 64 + lane] = acc[mb][nb][r];
+        q8s_lds[(((wave * MB + mb) * NB + nb) * 4 + r) * 64 + lane] = acc[mb][nb][r];
   __syncthreads();
   for (int e = threadIdx.x; e < MB * NB * 256; e += 64 * WAVES) {
     const int l = e & 63, r = (e >> 6) & 3, blk = e >> 8;
@@ -105,17 +152,17 @@ __global__ __launch_bounds__(64 * WAVES) void w8a8_small_kernel(const W8A8Args a
     if (m >= a.M || n >= a.N) continue;
     int sum = 0;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) sum += q8s_red[(((w * MB + mb) * NB + nb) * 4 + r) * 64 + l];
+    for (int w = 0; w < WAVES; ++w) sum += q8s_lds[(((w * MB + mb) * NB + nb) * 4 + r) * 64 + l];
     to_global(a.y)[static_cast<size_t>(m) * a.N + n] =
         f32_to_bf16_bits(static_cast<float>(sum) * (a.sx[m] * a.sw[n]));
   }
 }
 
-template <int MB, int NB, int WAVES, int P>
+template <int MB, int NB, int WAVES, bool XS>
 hipError_t launch_small(const W8A8Args& a, hipStream_t stream) {
   const int NCB = (a.N + 15) / 16;
-  const size_t lds = static_cast<size_t>(WAVES) * MB * NB * 1024;
-  const void* fn = reinterpret_cast<const void*>(&w8a8_small_kernel<MB, NB, WAVES, P>);
+  const size_t lds = static_cast<size_t>(WAVES) * MB * 1024 * (XS && NB < 2 ? 2 : NB);
+  const void* fn = reinterpret_cast<const void*>(&w8a8_small_kernel<MB, NB, WAVES, XS>);
   if (lds > 48 * 1024) {
     const hipError_t e =
         hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
@@ -129,28 +176,72 @@ hipError_t launch_small(const W8A8Args& a, hipStream_t stream) {
 
 // -------------------------------------------------------------- many rows
 
-constexpr int kT8KT = 128;               // k per k-tile
-constexpr int kT8Pieces = kT8KT / 16;    // 16-byte pieces of a row
-
-// LDS slot of piece p of a 128-byte row: conflict-free for the staging writes
-// (eight rows a wave) and the fragment reads (sixteen rows, one piece).
-__device__ __forceinline__ int t8_slot(int piece, int row) {
-  return piece ^ (row & 7) ^ ((row >> 3) & 1);
-}
+constexpr int kT8KT = 128;  // k per k-tile: two matrix-instruction steps
 
 template <int WM, int WN, int MB, int NB>
 struct T8Cfg {
-  static constexpr int Threads = 64 * WM * WN;
+  static constexpr int Waves = WM * WN;
+  static constexpr int Threads = 64 * Waves;
   static constexpr int Rows = WM * MB * 16;
-  static constexpr int Blocks = WN * NB;
-  static constexpr int Loads = Rows * kT8Pieces / Threads;
-  static constexpr int RowStep = Threads / kT8Pieces;
+  static constexpr int Blocks = WN * NB;                       // 16-column blocks
+  static constexpr int Pieces = Rows / 8 + Blocks * 2;         // 1 KB pieces of a k-tile
+  static constexpr int Loads = (Pieces + Waves - 1) / Waves;   // per wave
   static constexpr int ABytes = Rows * kT8KT;
-  static constexpr size_t Lds = 2 * static_cast<size_t>(ABytes);
+  static constexpr int BufBytes = ABytes + Blocks * 2048;
+  static constexpr size_t Lds = 2 * static_cast<size_t>(BufBytes);
+  static_assert(Lds <= 160 * 1024, "both buffers fit");
 };
 
+typedef int rsrc4 __attribute__((ext_vector_type(4)));
+
+// Buffer descriptor of [base, base + bytes); loads past the end do not fault.
+__device__ __forceinline__ rsrc4 raw_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t p = reinterpret_cast<uint64_t>(base);
+  rsrc4 r;
+  r[0] = uniform(static_cast<int>(p));
+  r[1] = uniform(static_cast<int>((p >> 32) & 0xFFFFu));
+  r[2] = uniform(static_cast<int>(bytes));
+  r[3] = 0x00020000;
+  return r;
+}
+
+// One wave's copy of 64 x 16 bytes from r + voff (per lane) to LDS bytes
+// lds .. lds + 1023 (lane l's at 16 l), without passing through registers.
+// In inline assembly because the compiler, which cannot tell these LDS bytes
+// from others, would wait for every such copy before the next LDS read; the
+// loops that use it hold every wait themselves.
+__device__ __forceinline__ void copy_to_lds(uint32_t lds, uint32_t voff, rsrc4 r) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, 0 offen lds"
+      :
+      : "s"(lds), "v"(voff), "s"(r)
+      : "memory");
+}
+
+// A workgroup's tile is (16 MB WM) rows x (16 NB WN) columns; k advances in
+// k-tiles of 128. Both operands of a k-tile are copied to one of two LDS
+// buffers: activation rows of 128 bytes with their 16-byte pieces permuted by
+// t8_slot on the way (the lanes read permuted addresses of the same cache
+// lines), weight tiles as they lie. Per k-tile a wave reads 2 (MB + NB)
+// operands for 2 MB NB matrix instructions, those of half a k-tile while the
+// half before it multiplies. The one barrier per k-tile sits between the
+// halves: behind it, every wave has read the current buffer, which is refilled
+// with the k-tile after next, and the next buffer, whose copies were issued
+// one k-tile earlier, is complete.
+//
+// Copies and operand reads are dealt out among the matrix instructions: issued
+// in one run, the copies queue up in front of the address unit (16 cycles for
+// each KB) and hold back the matrix instructions behind them. At M = 1024, N =
+// 34816, K = 5120, 256 x 192 tiles: 188 -> 173 us (2,110 TOP/s; a library
+// product of 8192^3 reaches 2,135 on the same card). There the matrix
+// instructions alone take 117 us and with the operand reads 135: the copies'
+// rate, about 20 bytes a cycle and compute unit, bounds the rest. Five
+// buffers in place of two, and copies through registers, were not faster (198
+// and 189 us).
 template <int WM, int WN, int MB, int NB>
-__global__ __launch_bounds__(64 * WM * WN, 8 / (WM * WN)) void w8a8_tile_kernel(const W8A8Args a, int MT, int NT) {
+__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void w8a8_tile_kernel(const W8A8Args a, int MT, int NT) {
   using C = T8Cfg<WM, WN, MB, NB>;
   extern __shared__ __attribute__((aligned(16))) unsigned char t8_lds[];
   const int tile = xcd_grouped(blockIdx.x, MT * NT);
@@ -160,45 +251,57 @@ __global__ __launch_bounds__(64 * WM * WN, 8 / (WM * WN)) void w8a8_tile_kernel(
   const int c16 = lane & 15, lg = lane >> 4;
   const int m0 = mt * C::Rows;
   const int S = (a.K + 63) / 64, NCB = (a.N + 15) / 16, KT = (a.K + kT8KT - 1) / kT8KT;
-  const int spiece = tid % kT8Pieces, srow0 = tid / kT8Pieces;
+  const int rows = min(a.M - m0, C::Rows);
 
+  // Piece i of a wave is piece wave + Waves i of the k-tile (past the last:
+  // the last again): 8 activation rows, or one block's weight tile of one
+  // step. Rows and blocks past the last repeat it (their results are not
+  // stored). What lies past the end of K is the next row's codes or zero, and
+  // meets zero weights; weight tiles past the last step are not used.
+  uint32_t off[C::Loads];
+#pragma unroll
+  for (int i = 0; i < C::Loads; ++i) {
+    const int c = min(wave + C::Waves * i, C::Pieces - 1);
+    if (c < C::Rows / 8) {
+      const int row = c * 8 + lane / 8;
+      off[i] = static_cast<uint32_t>(min(row, rows - 1)) * static_cast<uint32_t>(a.K) + t8_slot(lane & 7, row & 15) * 16;
+    } else {
+      const int b = c - C::Rows / 8;  // block b / 2, step b % 2
+      off[i] = (static_cast<uint32_t>(min(nt * C::Blocks + b / 2, NCB - 1)) * S + b % 2) * 1024u + lane * 16u;
+    }
+  }
   const uint8_t* xbase = a.xq + static_cast<size_t>(m0) * a.K;
-  const uint32_t xbytes = static_cast<uint32_t>(min(a.M - m0, C::Rows)) * static_cast<uint32_t>(a.K);
-  const __amdgpu_buffer_rsrc_t rq = make_rsrc(a.qweight, static_cast<uint32_t>(NCB) * static_cast<uint32_t>(S) * 1024u);
-  uint32_t boff[NB];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
-    boff[nb] = static_cast<uint32_t>(min((nt * C::Blocks + wn * NB + nb), NCB - 1)) * S * 1024u;
-
-  u32x4 sr[C::Loads];
-  auto stage_load = [&](int t) {
-    // rows past the last read as zero; so does a piece past the end of the
-    // tile's last row, and one past the end of another row holds the next
-    // row's codes, which meet zero weights
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(xbase + t * kT8KT, xbytes - static_cast<uint32_t>(t) * kT8KT);
-#pragma unroll
-    for (int i = 0; i < C::Loads; ++i)
-      sr[i] = __builtin_amdgcn_raw_buffer_load_b128(
-          rx, static_cast<uint32_t>(srow0 + i * C::RowStep) * a.K + spiece * 16, 0, 0);
-  };
-  auto stage_store = [&](int buf) {
+  const uint32_t xbytes = static_cast<uint32_t>(rows) * static_cast<uint32_t>(a.K);
+  const uint32_t wbytes = static_cast<uint32_t>(NCB) * static_cast<uint32_t>(S) * 1024u;
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+      (__attribute__((address_space(3))) unsigned char*)t8_lds));
+  // part g of G of k-tile t's copies
+  auto copy = [&](int t, int g, int G) {
+    const rsrc4 rx = raw_rsrc(xbase + static_cast<size_t>(t) * kT8KT, xbytes - static_cast<uint32_t>(t) * kT8KT);
+    const rsrc4 rw = raw_rsrc(a.qweight + static_cast<size_t>(t) * 2048, wbytes - static_cast<uint32_t>(t) * 2048u);
 #pragma unroll
     for (int i = 0; i < C::Loads; ++i) {
-      const int row = srow0 + i * C::RowStep;
-      *reinterpret_cast<u32x4*>(t8_lds + buf * C::ABytes + row * kT8KT + t8_slot(spiece, row) * 16) = sr[i];
+      if (i * G / C::Loads != g) continue;
+      const int c = min(wave + C::Waves * i, C::Pieces - 1);
+      copy_to_lds(lds0 + (t & 1) * C::BufBytes + c * 1024, off[i], c < C::Rows / 8 ? rx : rw);
     }
   };
-  struct B {
-    i32x4 w[2][NB];
+
+  struct Half {
+    i32x4 x[MB], w[NB];
   };
-  auto load_b = [&](B& b, int t) {
+  const unsigned char* const xfrag = t8_lds + (wm * MB * 16 + c16) * kT8KT;
+  const unsigned char* const wfrag = t8_lds + C::ABytes + wn * NB * 2048 + lane * 16;
+  // part g of G of the operands of half s of k-tile t
+  auto read = [&](Half& h, int t, int s, int g, int G) {
+    const int buf = (t & 1) * C::BufBytes;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int step = min(2 * t + s, S - 1);  // past the last: re-read, not used
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-        b.w[s][nb] = __builtin_bit_cast(
-            i32x4, __builtin_amdgcn_raw_buffer_load_b128(rq, lane * 16, static_cast<int>(boff[nb] + step * 1024u), 0));
+    for (int i = 0; i < MB + NB; ++i) {
+      if (i * G / (MB + NB) != g) continue;
+      if (i < NB)
+        h.w[i] = *reinterpret_cast<const i32x4*>(wfrag + buf + i * 2048 + s * 1024);
+      else
+        h.x[i - NB] = *reinterpret_cast<const i32x4*>(xfrag + buf + (i - NB) * 16 * kT8KT + t8_slot(4 * s + lg, c16) * 16);
     }
   };
   i32x4 acc[MB][NB];
@@ -206,62 +309,89 @@ __global__ __launch_bounds__(64 * WM * WN, 8 / (WM * WN)) void w8a8_tile_kernel(
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = i32x4{0, 0, 0, 0};
-  auto compute = [&](const B& b, int t, int buf) {
-    const unsigned char* base = t8_lds + buf * C::ABytes + (wm * MB * 16 + c16) * kT8KT;
+  auto multiply = [&](const Half& h, int mb) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (2 * t + s >= S) break;  // uniform
-      i32x4 af[MB];
+    for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = mfma_i8(h.w[nb], h.x[mb], acc[mb][nb]);
+  };
+
+  Half h0, h1;
+  copy(0, 0, 1);
+  wait_vmem_all();
+  lds_barrier();
+  if (KT > 1) copy(1, 0, 1);
+  read(h0, 0, 0, 0, 1);
+  auto tile_of = [&](int t, auto refill) {
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
-        af[mb] = *reinterpret_cast<const i32x4*>(base + mb * 16 * kT8KT + t8_slot(4 * s + lg, c16) * 16);
+    for (int g = 0; g < MB; ++g) {
+      read(h1, t, 1, g, MB);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(h0, g);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    wait_vmem_all();  // k-tile t + 1 has landed
+    lds_barrier();    // everywhere, and k-tile t has been read
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = mfma_i8(af[mb], b.w[s][nb], acc[mb][nb]);
+    for (int g = 0; g < MB; ++g) {
+      if constexpr (refill) copy(t + 2, g, MB);
+      read(h0, t + 1, 0, g, MB);         // past the last: not used
+      __builtin_amdgcn_sched_barrier(0);
+      if (2 * t + 1 < S) multiply(h1, g);  // else: the last k-tile has one step
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
+  int t = 0;
+  for (; t + 2 < KT; ++t) tile_of(t, std::true_type{});
+  for (; t < KT; ++t) tile_of(t, std::false_type{});
 
-  B b0, b1;
-  stage_load(0);
-  load_b(b0, 0);
-  stage_store(0);
-  lds_barrier();
-  auto iter = [&](int t, const B& cur, B& nxt) {
-    const int tn = t + 1 < KT ? t + 1 : t;
-    stage_load(tn);
-    load_b(nxt, tn);
-    __builtin_amdgcn_sched_barrier(0);  // issue the loads before the math
-    compute(cur, t, t & 1);
-    stage_store((t & 1) ^ 1);
-    lds_barrier();
-  };
-  for (int t = 0; t < KT; t += 2) {
-    iter(t, b0, b1);
-    if (t + 1 < KT) iter(t + 1, b1, b0);
-  }
-
-  gptr<uint16_t> yg = to_global(a.y);
-  float rs[MB][4];
+  // The accumulator of lane l holds columns 4 (l / 16) .. + 3 of row l % 16 of
+  // its block (the weights are the first operand), so four bf16 go to LDS at
+  // once; one row block at a time passes through the wave's own part of LDS
+  // and leaves as 16-byte stores of whole row pieces. (Two-byte stores from
+  // the registers, 32 bytes of a row together, took 23 us of 211 at M = 1024,
+  // N = 34816, K = 5120.)
+  __syncthreads();
+  constexpr int RowBytes = NB * 32, Stride = RowBytes + 16;  // padded against bank conflicts
+  static_assert(C::Waves * 16 * Stride <= static_cast<int>(C::Lds), "the wave parts fit");
+  unsigned char* const part = t8_lds + wave * (16 * Stride);
+  const int n0 = (nt * C::Blocks + wn * NB) * 16;  // the wave's first column
+  f32x4 cs[NB];
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb)
+  for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      rs[mb][r] = to_global(a.sx)[min(m0 + (wm * MB + mb) * 16 + 4 * lg + r, a.M - 1)];
+    for (int r = 0; r < 4; ++r) cs[nb][r] = to_global(a.sw)[min(n0 + nb * 16 + 4 * lg + r, a.N - 1)];
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    const int col = (nt * C::Blocks + wn * NB + nb) * 16 + c16;
-    if (col >= a.N) continue;
-    const float cs = to_global(a.sw)[col];
+  for (int mb = 0; mb < MB; ++mb) {
+    const int row0 = m0 + (wm * MB + mb) * 16;
+    const float rs = to_global(a.sx)[min(row0 + c16, a.M - 1)];
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
+    for (int nb = 0; nb < NB; ++nb) {
+      u32x2 o;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = m0 + (wm * MB + mb) * 16 + 4 * lg + r;
-        if (row < a.M)
-          yg[static_cast<size_t>(row) * a.N + col] =
-              f32_to_bf16_bits(static_cast<float>(acc[mb][nb][r]) * (rs[mb][r] * cs));
+      for (int q = 0; q < 2; ++q) {
+        const float lo = static_cast<float>(acc[mb][nb][2 * q]) * (rs * cs[nb][2 * q]);
+        const float hi = static_cast<float>(acc[mb][nb][2 * q + 1]) * (rs * cs[nb][2 * q + 1]);
+        o[q] = f32_to_bf16_bits(lo) | static_cast<uint32_t>(f32_to_bf16_bits(hi)) << 16;
       }
+      *reinterpret_cast<u32x2*>(part + c16 * Stride + nb * 32 + lg * 8) = o;
+    }
+    if (a.N % 8 == 0) {  // rows keep 16-byte alignment, pieces are in or out whole
+      constexpr int Pieces = NB * 2;  // per row
+#pragma unroll
+      for (int i = 0; i < (16 * Pieces + 63) / 64; ++i) {
+        const int e = i * 64 + lane, row = e / Pieces, col = e % Pieces * 8;
+        if (e >= 16 * Pieces) continue;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(part + row * Stride + col * 2);
+        if (row0 + row < a.M && n0 + col < a.N)
+          *reinterpret_cast<gptr<u32x4>>(to_global(a.y) + static_cast<size_t>(row0 + row) * a.N + n0 + col) = v;
+      }
+    } else {
+      for (int e = lane; e < 16 * NB * 16; e += 64) {
+        const int row = e / (NB * 16), col = e % (NB * 16);
+        const uint16_t v = *reinterpret_cast<const uint16_t*>(part + row * Stride + col * 2);
+        if (row0 + row < a.M && n0 + col < a.N)
+          to_global(a.y)[static_cast<size_t>(row0 + row) * a.N + n0 + col] = v;
+      }
+    }
   }
 }
 
@@ -282,13 +412,68 @@ hipError_t launch_tile(const W8A8Args& a, hipStream_t stream) {
   return hipLaunchKernel(fn, dim3(static_cast<unsigned>(blocks)), dim3(C::Threads), kargs, C::Lds, stream);
 }
 
+// The forms, by modelled time. Few rows: a workgroup streams its 16 (rows +
+// columns) x K operand bytes at about 45 GB/s after 2.5 us (a fifth less from
+// three workgroups per compute unit on), one round of workgroups after the
+// other, so the smallest rounds x (row blocks + column blocks) is best; where
+// the workgroups are few (a narrow N), one column block and 16 waves. Tiles:
+// per k-tile of 128 the n tiles of a compute unit take 0.6 us or 0.3 n (64 x
+// 64), 0.9 or 0.75 n (128 x 192, two workgroups at once) and 1.3 n (256 x 192). Measured on N x K =
+// 7168 x 5120, 5120 x 6144, 34816 x 5120, 5120 x 17408 and their eighths at M
+// = 1 to 2048 with every form; the one chosen is within 1.09 of the fastest
+// measured, mostly the fastest. For instance (us): 7168 x 5120, M = 128: 4 x 2
+// 25.3, 64 x 64 26.9, 128 x 192 37.1; M = 256: 64 x 64 28.3, 128 x 192 37.2;
+// 34816 x 5120, M = 64: 4 x 2 60.6, 64 x 64 41.3, 128 x 192 44.8; M = 512: 128
+// x 192 104, 256 x 192 106; M = 1024: 183, 161.
+enum W8A8Form : int { kS1x1, kS1x2, kS2x1, kS2x2, kS4x2, kS2x4, kT64x64, kT128x192, kT256x192 };
+constexpr int kSmallMaxRows = 512;  // few-rows forms are not looked at above
+
+W8A8Form w8a8_form(int M, int N, int K) {
+  auto rounds = [&](long long rows, long long cols) {
+    const long long tiles = (M + rows - 1) / rows * ((N + cols - 1) / cols);
+    return static_cast<double>((tiles + kModelCUs - 1) / kModelCUs);
+  };
+  const double kt = (K + kT8KT - 1) / kT8KT;
+  const double r64 = rounds(64, 64), r128 = rounds(128, 192), r256 = rounds(256, 192);
+  W8A8Form best = kT64x64;
+  double t = 1.0 + kt * (0.3 * r64 > 0.6 ? 0.3 * r64 : 0.6);
+  auto consider = [&](W8A8Form f, double us) {
+    if (us < t) {
+      best = f;
+      t = us;
+    }
+  };
+  consider(kT128x192, 1.0 + kt * (0.75 * r128 > 0.9 ? 0.75 * r128 : 0.9));
+  consider(kT256x192, 1.0 + kt * 1.3 * r256);
+  if (M <= kSmallMaxRows) {
+    const struct {
+      W8A8Form f;
+      int mb, nb;
+    } small[] = {{kS4x2, 4, 2}, {kS2x4, 2, 4}, {kS2x2, 2, 2}, {kS2x1, 2, 1}, {kS1x2, 1, 2}, {kS1x1, 1, 1}};
+    for (const auto& s : small) {  // of equal ones the first: fewest reads of the weights
+      const double r = rounds(16 * s.mb, 16 * s.nb);
+      consider(s.f, 2.5 + r * (r >= 3 ? 1.2 : 1.0) * (s.mb + s.nb) * 16.0 * K / 45000.0);
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
 hipError_t launch_w8a8(const W8A8Args& a, hipStream_t stream) {
-  if (a.M <= 16) return launch_small<1, 2, 8, 2>(a, stream);
-  if (a.M <= 32) return launch_small<2, 2, 8, 2>(a, stream);
-  if (a.M <= 128) return launch_small<4, 2, 8, 2>(a, stream);
-  return launch_tile<2, 4, 8, 4>(a, stream);
+  switch (w8a8_form(a.M, a.N, a.K)) {
+    case kS1x1: return launch_small<1, 1, 16, true>(a, stream);
+    // read in operand order up to 8 rows: 7.9 against 8.0 us at M = 1, N =
+    // 7168, K = 5120, 4.7 against 5.9 at N = 896; at 16 rows 9.4 against 9.1
+    case kS1x2: return a.M <= 8 ? launch_small<1, 2, 8, false>(a, stream) : launch_small<1, 2, 8, true>(a, stream);
+    case kS2x1: return launch_small<2, 1, 16, true>(a, stream);
+    case kS2x2: return launch_small<2, 2, 8, true>(a, stream);
+    case kS4x2: return launch_small<4, 2, 8, true>(a, stream);
+    case kS2x4: return launch_small<2, 4, 8, true>(a, stream);
+    case kT64x64: return launch_tile<2, 2, 2, 2>(a, stream);
+    case kT128x192: return launch_tile<2, 4, 4, 3>(a, stream);
+    default: return launch_tile<4, 2, 4, 6>(a, stream);
+  }
 }
 
 }  // namespace w4a16_internal
