@@ -125,6 +125,28 @@ def test_shared_rows(T, k, E, swiglu):
     check(E, 64, 256, 128, ids, k, swiglu, seed=T)
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("swiglu,N", [(False, 5000), (False, 5003), (True, 9952)])
+def test_tall_tiles(group, swiglu, N):
+    """Enough rows and columns for 128-row tiles, with experts of every tail: one
+    row, up to 32, 64 and 128 rows past whole tiles, none."""
+    rng = np.random.default_rng(group)
+    count = [1, 0, 128, 129, 257 + 31, 384 + 33, 512 + 64, 512 + 65, 512 + 127, 640, 30, 3]
+    ids = np.concatenate([np.full(c, e) for e, c in enumerate(count)] + [np.full(800, 4)])
+    check(len(count), N, 256 + group, group, rng.permutation(ids), 1, swiglu, seed=group)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128, 256])
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("T,N", [(1, 2048), (8, 4096), (40, 2048)])
+def test_deep_products_of_few_rows(group, swiglu, T, N):
+    """The K-splitting form at both widths, tiles of at most 4 rows, up to 16 and past 16."""
+    rng = np.random.default_rng(T)
+    ids = np.concatenate([rng.permutation(10)[:8] for _ in range(T)])
+    ids[rng.random(ids.size) < 0.3] = 1  # one expert past 16 rows at 40 tokens
+    check(10, N, 2560, group, ids, 8, swiglu, seed=T)
+
+
 def test_one_expert_takes_all_and_others_none():
     for slots in (5, 100, 900):
         check(4, 64, 256, 128, np.full(slots, 2), 1, False)

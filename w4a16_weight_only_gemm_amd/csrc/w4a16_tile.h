@@ -145,12 +145,14 @@ struct TileEngine {
   // ---- activation staging: thread stages piece tid % 16 (8 values) of rows
   // tid / 16 + 32 i, through a buffer resource based at (row m0, k of the
   // k-tile) and ending at the end of x, so rows beyond M read as zero ----
-  __device__ __forceinline__ void stage_load(StageRegs<GS, MB>& r, int t) const {
+  __device__ __forceinline__ void stage_load(StageRegs<GS, MB>& r, int t, int i0 = 0,
+                                             int i1 = C::Loads) const {
     const __amdgpu_buffer_rsrc_t rx =
         make_rsrc(xrow0 + t * kLgKT, xbytes - static_cast<uint32_t>(t) * (kLgKT * 2));
     const int spiece = tid % kLgPieces, srow0 = tid / kLgPieces;
 #pragma unroll
     for (int i = 0; i < C::Loads; ++i) {
+      if (i < i0 || i >= i1) continue;
       uint32_t off;
       if constexpr (GATHER)
         off = voff[i];
@@ -174,7 +176,7 @@ struct TileEngine {
   }
 
   // ---- this wave's weights and scales of k-tile t ----
-  __device__ __forceinline__ void load_b(BRegs<GS>& r, int t) const {
+  __device__ __forceinline__ void load_b(BRegs<GS>& r, int t, int nb0 = 0, int nb1 = kLgNB) const {
     const uint32_t qlane = static_cast<uint32_t>(lane) * C::WPL * 4u;
     const uint32_t slane = static_cast<uint32_t>(lane & 14) * 2u;
 #pragma unroll
@@ -183,6 +185,7 @@ struct TileEngine {
       if (grp > G - 1) grp = G - 1;
 #pragma unroll
       for (int nb = 0; nb < kLgNB; ++nb) {
+        if (nb < nb0 || nb >= nb1) continue;
         const uint32_t tile_idx = static_cast<uint32_t>(blk[nb]) * G + grp;
         const int qoff = static_cast<int>(tile_idx * (64u * C::WPL * 4u));
         if constexpr (C::WPL == 4) {
@@ -205,8 +208,10 @@ struct TileEngine {
   // One k-tile: 4 MFMA steps of 32 k. Step st belongs to group st / WPL of the
   // k-tile; a group's accumulation starts from its -24 * row-sum tile and
   // ends with the scaled add into acc_out.
-  __device__ __forceinline__ void compute(Acc<MB>& acc_out, const BRegs<GS>& b, int t,
-                                          int buf) const {
+  // after(st) runs behind step st's MFMAs.
+  template <typename F>
+  __device__ __forceinline__ void compute(Acc<MB>& acc_out, const BRegs<GS>& b, int t, int buf,
+                                          F after) const {
     const unsigned char* base = lds + buf * C::BufBytes;
     const float* sums = reinterpret_cast<const float*>(base + C::ABytes);
     const int arow = lane & 15, jgrp = lane >> 4;
@@ -243,6 +248,7 @@ struct TileEngine {
         for (int nb = 0; nb < kLgNB; ++nb)
           acc[nb][mb] = mfma16(af[mb], bq[nb], w == 0 ? bias[mb] : acc[nb][mb]);
       __builtin_amdgcn_sched_barrier(0);
+      after(st);
       if (w == C::WPL - 1) {
 #pragma unroll
         for (int nb = 0; nb < kLgNB; ++nb) {
@@ -252,6 +258,11 @@ struct TileEngine {
         }
       }
     }
+  }
+
+  __device__ __forceinline__ void compute(Acc<MB>& acc_out, const BRegs<GS>& b, int t,
+                                          int buf) const {
+    compute(acc_out, b, t, buf, [](int) {});
   }
 
   // k-tiles [k0, k1): k-tile t computes from LDS buffer (t - k0) & 1 while
@@ -273,6 +284,36 @@ struct TileEngine {
       load_b(nxt, tn);
       __builtin_amdgcn_sched_barrier(0);       // issue the loads before the math
       compute(acc, cur, t, buf);
+      stage_store(sr, buf ^ 1);
+      lds_barrier();
+    };
+    for (int t = k0; t < k1; t += 2) {
+      iter(t, b0, b1);
+      if (t + 1 >= k1) break;
+      iter(t + 1, b1, b0);
+    }
+  }
+
+  // kloop with the weights' loads behind the MFMA runs of the first two steps:
+  // issued in one run with the activations', they queue up in front of the
+  // address unit and hold back the MFMAs behind them (experts' products, 256
+  // rows each of 128 experts, N = 2048, K = 5120: 842 -> 810 us).
+  __device__ __forceinline__ void kloop_spread(Acc<MB>& acc, int k0, int k1) const {
+    StageRegs<GS, MB> sr;
+    BRegs<GS> b0, b1;
+    stage_load(sr, k0);
+    load_b(b0, k0);
+    stage_store(sr, 0);
+    lds_barrier();
+    auto iter = [&](int t, const BRegs<GS>& cur, BRegs<GS>& nxt) {
+      const int tn = t + 1 < k1 ? t + 1 : t;   // the last iteration reloads (unused)
+      const int buf = (t - k0) & 1;
+      stage_load(sr, tn);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(acc, cur, t, buf, [&](int st) {
+        if (st == 0) load_b(nxt, tn, 0, 1);
+        if (st == 1) load_b(nxt, tn, 1, 2);
+      });
       stage_store(sr, buf ^ 1);
       lds_barrier();
     };
