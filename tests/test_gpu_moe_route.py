@@ -222,3 +222,25 @@ def test_binding_refuses_wrong_tensors():
         with pytest.raises(ValueError):
             call(**kw)
     assert math.isfinite(float(f.sum()))
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("gap", [0.0, 1e-9, 3e-8, 1e-6, 1e-4])
+def test_values_next_to_each_other(scoring, gap):
+    """Choice values nearer than fp32 resolves (and some that it does): a logit's
+    last bits and a bias that nearly makes up for them decide as in 64 bits."""
+    rng = np.random.default_rng(2)
+    T, E = 300, 96
+    z = np.round(rng.standard_normal((T, E)) * 4).astype(np.float32) / 4
+    z = np.nextafter(z, np.where(rng.random((T, E)) < 0.5, np.inf, -np.inf).astype(np.float32))
+    b = np.where(rng.random(E) < 0.5, gap, 0.0)
+    for kw in (dict(), dict(groups=8, groups_kept=3, group_top=2)):
+        check_route(z, b, 8, scoring=scoring, **kw)
+
+
+@pytest.mark.parametrize("bias", [1e30, -1e30, 1000.0])
+def test_large_biases(bias):
+    rng = np.random.default_rng(4)
+    b = np.where(rng.random(64) < 0.4, bias, 0.1)
+    check_route(rng.standard_normal((50, 64)).astype(np.float32), b, 6, scoring="sigmoid")
+    check_route(rng.standard_normal((50, 64)).astype(np.float32) * 60, b, 6, groups=4, groups_kept=2)

@@ -4,11 +4,12 @@ are re-exported by the package."""
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import numpy as np
 
-from . import (W4A16_ERR_INVALID_ARG, W4A16_OK, W4A16Error, _check_sizes, _lib, _ptr, _stream,
-               _torch, w4a16_qweight_bytes, w4a16_scales_bytes)
+from . import (W4A16_ERR_INVALID_ARG, W4A16_OK, W4A16Error, _lib, _ptr, _stream, _torch,
+               w4a16_qweight_bytes, w4a16_scales_bytes)
 
 W4A16_ROUTE_MAX_EXPERTS = 1024
 W4A16_ROUTE_MAX_TOP_K = 32
@@ -46,13 +47,50 @@ for _name, (_res, _args) in MOE_SIGNATURES.items():
     _fn.argtypes = _args
 
 
-def _check_types(**need):
-    """name=(tensor or address, torch dtype name): dtype checks for torch tensors."""
-    if _torch is None:
-        return
-    for name, (t, dtype) in need.items():
-        if isinstance(t, _torch.Tensor) and t.dtype != getattr(_torch, dtype):
-            raise TypeError(f"{name} must be torch.{dtype}")
+if _torch is not None:
+    _Tensor, _F32, _BF16 = _torch.Tensor, _torch.float32, _torch.bfloat16
+    _I32, _I8 = _torch.int32, _torch.int8
+    _raw_stream = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+else:  # pragma: no cover - torch is optional for host-only use
+    _Tensor, _F32, _BF16, _I32, _I8, _raw_stream = (), None, None, None, None, None
+
+
+def _device() -> int:
+    """The current device's index, or -2 where no device tensor can exist yet."""
+    if _torch is None or not _torch.cuda.is_initialized():
+        return -2
+    return _torch.cuda.current_device()
+
+
+def _at(name: str, t, dtype, nbytes: int, dev: int):
+    """Address of a buffer: a raw address or None as it is, a tensor after its checks
+    (any dtype where `dtype` is None). A few hundred nanoseconds each: small calls
+    are bound by the host."""
+    if isinstance(t, _Tensor):
+        if dtype is not None and t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on the current device")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.nbytes < nbytes:
+            raise ValueError(f"{name} holds {t.nbytes} bytes, needs {nbytes}")
+        return t.data_ptr()
+    if t is None or isinstance(t, int):
+        return t
+    raise TypeError(f"unsupported buffer type {type(t)} for {name}")
+
+
+def _on(stream, dev: int):
+    """Address of the stream: the given one, else torch's current stream of `dev`."""
+    if stream is None and dev >= 0 and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
+
+
+@functools.lru_cache(maxsize=256)
+def _config(*fields) -> w4a16_route_config:
+    return w4a16_route_config(*fields)
 
 
 def w4a16_moe_route_workspace_bytes(T: int, experts: int) -> int:
@@ -77,26 +115,28 @@ def w4a16_moe_route(logits, bias, T: int, E: int, top_k: int, ids, weights, offs
     (float32 or bfloat16; `logits_type` is needed for a raw address only). bias and, where
     w4a16_moe_route_workspace_bytes is 0, workspace may be None."""
     if logits_type is None:
-        if _torch is None or not isinstance(logits, _torch.Tensor):
+        if not isinstance(logits, _Tensor):
             raise TypeError("logits_type is needed for a raw address")
-        if logits.dtype not in (_torch.float32, _torch.bfloat16):
+        if logits.dtype is _F32:
+            logits_type = W4A16_LOGITS_F32
+        elif logits.dtype is _BF16:
+            logits_type = W4A16_LOGITS_BF16
+        else:
             raise TypeError("logits must be torch.float32 or torch.bfloat16")
-        logits_type = W4A16_LOGITS_BF16 if logits.dtype == _torch.bfloat16 else W4A16_LOGITS_F32
-    elif logits_type in (W4A16_LOGITS_F32, W4A16_LOGITS_BF16):
-        _check_types(logits=(logits,
-                             "bfloat16" if logits_type == W4A16_LOGITS_BF16 else "float32"))
-    _check_types(bias=(bias, "float32"), ids=(ids, "int32"), weights=(weights, "float32"),
-                 offsets=(offsets, "int32"), rows=(rows, "int32"))
-    size = 2 if logits_type == W4A16_LOGITS_BF16 else 4
-    _check_sizes(logits=(logits, size * T * E), bias=(bias, 4 * E), ids=(ids, 4 * T * top_k),
-                 weights=(weights, 4 * T * top_k), offsets=(offsets, 4 * (E + 1)),
-                 rows=(rows, 4 * T * top_k))
+    bf16 = logits_type == W4A16_LOGITS_BF16
+    dev = _device()
+    places = 4 * T * top_k
     if workspace_bytes is None:
-        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    config = w4a16_route_config(E, top_k, scoring, logits_type, groups, groups_kept, group_top,
-                                int(bool(renormalize)), scale)
-    rc = moe_route_status(logits, bias, config, T, ids, weights, offsets, rows, workspace,
-                          workspace_bytes, stream)
+        workspace_bytes = workspace.nbytes if isinstance(workspace, _Tensor) else 0
+    rc = _lib.w4a16_moe_route(
+        _at("logits", logits, _BF16 if bf16 else _F32, (2 if bf16 else 4) * T * E, dev),
+        _at("bias", bias, _F32, 4 * E, dev),
+        ctypes.addressof(_config(E, top_k, scoring, logits_type, groups, groups_kept, group_top,
+                                 1 if renormalize else 0, scale)),
+        T, _at("ids", ids, _I32, places, dev), _at("weights", weights, _F32, places, dev),
+        _at("offsets", offsets, _I32, 4 * (E + 1), dev), _at("rows", rows, _I32, places, dev),
+        _at("workspace", workspace, None, workspace_bytes, dev), workspace_bytes,
+        _on(stream, dev))
     if rc != W4A16_OK:
         raise W4A16Error(rc, "w4a16_moe_route")
 
@@ -114,16 +154,19 @@ def w4a16_gemm_experts(x, qweight, scales, y, rows, offsets, slots: int, experts
                        stream=None) -> None:
     """Every expert's W4A16 product over the slots listed for it: y[s] = x[s // x_div] .
     dequant(weights of the expert), with W4A16_ACT_SWIGLU silu(gate) * up."""
-    _check_types(x=(x, "bfloat16"), y=(y, "bfloat16"), rows=(rows, "int32"),
-                 offsets=(offsets, "int32"))
-    if group > 0 and K % group == 0 and x_div > 0 and slots >= 0:
-        out = N // 2 if act == W4A16_ACT_SWIGLU else N
-        _check_sizes(x=(x, 2 * -(-slots // x_div) * K), y=(y, 2 * slots * out),
-                     qweight=(qweight, experts * w4a16_qweight_bytes(N, K)),
-                     scales=(scales, experts * w4a16_scales_bytes(N, K, group)),
-                     rows=(rows, 4 * slots), offsets=(offsets, 4 * (experts + 1)))
-    rc = gemm_experts_status(x, qweight, scales, y, rows, offsets, slots, experts, x_div, N, K,
-                             group, act, stream)
+    dev = _device()
+    xb = yb = qb = sb = 0
+    if group > 0 and K % group == 0 and x_div > 0:
+        xb = 2 * -(-slots // x_div) * K
+        yb = 2 * slots * (N // 2 if act == W4A16_ACT_SWIGLU else N)
+        qb = experts * w4a16_qweight_bytes(N, K)
+        sb = experts * w4a16_scales_bytes(N, K, group)
+    rc = _lib.w4a16_gemm_experts(
+        _at("x", x, _BF16, xb, dev), _at("qweight", qweight, None, qb, dev),
+        _at("scales", scales, None, sb, dev), _at("y", y, _BF16, yb, dev),
+        _at("rows", rows, _I32, 4 * slots, dev),
+        _at("offsets", offsets, _I32, 4 * (experts + 1), dev), slots, experts, x_div, N, K, group,
+        act, _on(stream, dev))
     if rc != W4A16_OK:
         raise W4A16Error(rc, "w4a16_gemm_experts")
 
@@ -137,11 +180,12 @@ def moe_combine_status(y, ids, weights, base, out, T, top_k, N, stream=None) -> 
 def w4a16_moe_combine(y, ids, weights, base, out, T: int, top_k: int, N: int,
                       stream=None) -> None:
     """out[T][N] = base (None: 0) + weighted sum of each token's top_k rows of y."""
-    _check_types(y=(y, "bfloat16"), base=(base, "bfloat16"), out=(out, "bfloat16"),
-                 ids=(ids, "int32"), weights=(weights, "float32"))
-    _check_sizes(y=(y, 2 * T * top_k * N), base=(base, 2 * T * N), out=(out, 2 * T * N),
-                 ids=(ids, 4 * T * top_k), weights=(weights, 4 * T * top_k))
-    rc = moe_combine_status(y, ids, weights, base, out, T, top_k, N, stream)
+    dev = _device()
+    row, places = 2 * T * N, 4 * T * top_k
+    rc = _lib.w4a16_moe_combine(
+        _at("y", y, _BF16, row * top_k, dev), _at("ids", ids, _I32, places, dev),
+        _at("weights", weights, _F32, places, dev), _at("base", base, _BF16, row, dev),
+        _at("out", out, _BF16, row, dev), T, top_k, N, _on(stream, dev))
     if rc != W4A16_OK:
         raise W4A16Error(rc, "w4a16_moe_combine")
 
@@ -179,10 +223,11 @@ def w8a8_gemm_status(xq, sx, qweight, scales, y, M, N, K, stream=None) -> int:
 def w8a8_gemm(xq, sx, qweight, scales, y, M: int, N: int, K: int, stream=None) -> None:
     """y[M][N] (bf16) = 8-bit integer product of the codes and row scales written by
     w4a8_quantize and the weights written by w8a8_pack, with fp32 scales per column."""
-    _check_types(xq=(xq, "int8"), sx=(sx, "float32"), scales=(scales, "float32"),
-                 y=(y, "bfloat16"))
-    _check_sizes(xq=(xq, M * K), sx=(sx, 4 * M), y=(y, 2 * M * N), scales=(scales, 4 * N),
-                 qweight=(qweight, w8a8_qweight_bytes(N, K)))
-    rc = w8a8_gemm_status(xq, sx, qweight, scales, y, M, N, K, stream)
+    dev = _device()
+    rc = _lib.w8a8_gemm(
+        _at("xq", xq, _I8, M * K, dev), _at("sx", sx, _F32, 4 * M, dev),
+        _at("qweight", qweight, None, w8a8_qweight_bytes(N, K), dev),
+        _at("scales", scales, _F32, 4 * N, dev), _at("y", y, _BF16, 2 * M * N, dev), M, N, K,
+        _on(stream, dev))
     if rc != W4A16_OK:
         raise W4A16Error(rc, "w8a8_gemm")

@@ -60,7 +60,7 @@ int w4a16_moe_route(const void* logits, const float* bias, const w4a16_route_con
   a.weights = weights;
   a.offsets = offsets;
   a.rows = rows;
-  a.hist = static_cast<int*>(workspace);
+  a.workspace = workspace;
   a.T = T;
   a.E = c->experts;
   a.top_k = c->top_k;

@@ -17,10 +17,17 @@ struct RouteArgs {
   float* weights;      // [T][top_k]
   int* offsets;        // [E + 1]
   int* rows;           // [T * top_k]
-  int* hist;           // workspace: [chunks][E] counts, then [E] totals
+  void* workspace;
+  uint8_t* counts;     // workspace: [chunks][E rounded up to 4] slots per expert
+  int* sums;           // workspace: [chunks + 1][E] of the chunks before
   int T, E, top_k;
   int sigmoid, bf16, groups, groups_kept, group_top, renormalize;
   float scale;
+  // filled in by launch_route
+  int per;             // experts per group
+  uint32_t per_inverse;  // floor(e / per) = high half of e * per_inverse
+  int group_lanes;     // lanes that look at a group, a power of two
+  int group_whole;     // a group's experts are exactly those its lanes hold
   int chunk;           // tokens per workgroup
   int chunks;
 };
