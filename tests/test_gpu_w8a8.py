@@ -71,7 +71,7 @@ def test_depths(M, K):
 @pytest.mark.parametrize("M,N,K", [
     (1, 200, 1040), (5, 5000, 656), (12, 5000, 656),          # one row block by one and two
     (120, 800, 1040), (30, 7000, 656),                        # two row blocks by one and two
-    (60, 7000, 656), (90, 5000, 1040),                        # four by two, two by four
+    (60, 7000, 656), (60, 5000, 1040), (90, 5000, 1040),      # four by two, two by three and four
     (520, 1000, 272), (1100, 2950, 144), (1090, 2957, 208),   # tiles of 64 x 64 and 128 x 192
     (4000, 2950, 144), (3970, 2941, 272), (4090, 2944, 64)])  # 256 x 192
 def test_every_form(M, N, K):

@@ -357,7 +357,7 @@ hipError_t launch_small_t(const ExpertsArgs& a, hipStream_t stream) {
   size_t lds = static_cast<size_t>(WAVES) * MB * NB * 1024;
   if (XS) lds += static_cast<size_t>(WAVES) * MB * 16 * 256;
   const void* fn = reinterpret_cast<const void*>(&experts_small_kernel<GS, MB, NB, WAVES, P4, P16, XS, ACT>);
-  if (lds > 48 * 1024) {
+  if (lds > 64 * 1024) {
     const hipError_t e =
         hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
     if (e != hipSuccess) return e;
@@ -486,9 +486,11 @@ hipError_t launch_tile_t(const ExpertsArgs& a, hipStream_t stream) {
   const long long blocks = row_tiles * NT;
   if (blocks * kLgThreads > 0xFFFFFFFFLL) return hipErrorInvalidValue;
   const void* fn = reinterpret_cast<const void*>(&experts_tile_kernel<GS, MB, ACT>);
-  const hipError_t e =
-      hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Lds));
-  if (e != hipSuccess) return e;
+  if (Lds > 64 * 1024) {
+    const hipError_t e =
+        hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Lds));
+    if (e != hipSuccess) return e;
+  }
   ExpertsArgs args = a;
   void* kargs[] = {&args, &NT};
   return hipLaunchKernel(fn, dim3(static_cast<unsigned>(blocks)), dim3(kLgThreads), kargs, Lds, stream);

@@ -49,12 +49,15 @@ __device__ __forceinline__ int t8_slot(int piece, int row) {
 // wave-private LDS area; read in operand order, a load's 16 consecutive lanes
 // sit in 16 rows, 16 cache lines for 256 bytes.
 template <int MB, int NB, int WAVES, bool XS>
-__global__ __launch_bounds__(64 * WAVES) void w8a8_small_kernel(const W8A8Args a) {
+__global__ __launch_bounds__(64 * WAVES) void w8a8_small_kernel(const W8A8Args a, int MT) {
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
   const int c16 = lane & 15, lg = lane >> 4;
   const int S = (a.K + 63) / 64, S2 = (S + 1) / 2, NCB = (a.N + 15) / 16;
-  const int b0 = blockIdx.x * NB, m0 = blockIdx.y * 16 * MB;
+  // row tiles of a column tile side by side on one XCD: its L2 serves the
+  // others (5120 x 17408, M = 128: 59.7 -> 51.1 us)
+  const int tile = xcd_grouped(blockIdx.x, gridDim.x);
+  const int b0 = tile / MT * NB, m0 = tile % MT * 16 * MB;
   const int s0 = static_cast<int>(static_cast<long long>(S2) * wave / WAVES);
   const int s1 = static_cast<int>(static_cast<long long>(S2) * (wave + 1) / WAVES);
   extern __shared__ __attribute__((aligned(16))) int q8s_lds[];  // operands, then the waves' sums
@@ -163,15 +166,15 @@ hipError_t launch_small(const W8A8Args& a, hipStream_t stream) {
   const int NCB = (a.N + 15) / 16;
   const size_t lds = static_cast<size_t>(WAVES) * MB * 1024 * (XS && NB < 2 ? 2 : NB);
   const void* fn = reinterpret_cast<const void*>(&w8a8_small_kernel<MB, NB, WAVES, XS>);
-  if (lds > 48 * 1024) {
+  if (lds > 64 * 1024) {
     const hipError_t e =
         hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
     if (e != hipSuccess) return e;
   }
   W8A8Args args = a;
-  void* kargs[] = {&args};
-  return hipLaunchKernel(fn, dim3((NCB + NB - 1) / NB, (a.M + 16 * MB - 1) / (16 * MB)),
-                         dim3(64 * WAVES), kargs, lds, stream);
+  int MT = (a.M + 16 * MB - 1) / (16 * MB);
+  void* kargs[] = {&args, &MT};
+  return hipLaunchKernel(fn, dim3((NCB + NB - 1) / NB * MT), dim3(64 * WAVES), kargs, lds, stream);
 }
 
 // -------------------------------------------------------------- many rows
@@ -404,9 +407,11 @@ hipError_t launch_tile(const W8A8Args& a, hipStream_t stream) {
   const long long blocks = static_cast<long long>(MT) * NT;
   if (blocks * C::Threads > 0xFFFFFFFFLL) return hipErrorInvalidValue;
   const void* fn = reinterpret_cast<const void*>(&w8a8_tile_kernel<WM, WN, MB, NB>);
-  const hipError_t e =
-      hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::Lds));
-  if (e != hipSuccess) return e;
+  if (C::Lds > 64 * 1024) {
+    const hipError_t e =
+        hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::Lds));
+    if (e != hipSuccess) return e;
+  }
   W8A8Args args = a;
   void* kargs[] = {&args, &MT, &NT};
   return hipLaunchKernel(fn, dim3(static_cast<unsigned>(blocks)), dim3(C::Threads), kargs, C::Lds, stream);
@@ -415,17 +420,17 @@ hipError_t launch_tile(const W8A8Args& a, hipStream_t stream) {
 // The forms, by modelled time. Few rows: a workgroup streams its 16 (rows +
 // columns) x K operand bytes at about 45 GB/s after 2.5 us (a fifth less from
 // three workgroups per compute unit on), one round of workgroups after the
-// other, so the smallest rounds x (row blocks + column blocks) is best; where
-// the workgroups are few (a narrow N), one column block and 16 waves. Tiles:
+// other, so the smallest rounds x (rows + columns) is best; where the
+// workgroups are few (a narrow N), one column block and 16 waves. Tiles:
 // per k-tile of 128 the n tiles of a compute unit take 0.6 us or 0.3 n (64 x
 // 64), 0.9 or 0.75 n (128 x 192, two workgroups at once) and 1.3 n (256 x 192). Measured on N x K =
 // 7168 x 5120, 5120 x 6144, 34816 x 5120, 5120 x 17408 and their eighths at M
-// = 1 to 2048 with every form; the one chosen is within 1.09 of the fastest
-// measured, mostly the fastest. For instance (us): 7168 x 5120, M = 128: 4 x 2
-// 25.3, 64 x 64 26.9, 128 x 192 37.1; M = 256: 64 x 64 28.3, 128 x 192 37.2;
+// = 1 to 2048 with every form; the one chosen is within 1.1 of the fastest
+// measured, mostly the fastest (1.3 once: 5120 x 2176, M = 128). For instance (us): 7168 x 5120, M = 128: 4 x 2
+// 23.1, 64 x 64 26.9, 128 x 192 37.1; M = 256: 64 x 64 28.3, 128 x 192 37.2;
 // 34816 x 5120, M = 64: 4 x 2 60.6, 64 x 64 41.3, 128 x 192 44.8; M = 512: 128
 // x 192 104, 256 x 192 106; M = 1024: 183, 161.
-enum W8A8Form : int { kS1x1, kS1x2, kS2x1, kS2x2, kS4x2, kS2x4, kT64x64, kT128x192, kT256x192 };
+enum W8A8Form : int { kS1x1, kS1x2, kS2x1, kS2x2, kS2x3, kS4x2, kS2x4, kT64x64, kT128x192, kT256x192 };
 constexpr int kSmallMaxRows = 512;  // few-rows forms are not looked at above
 
 W8A8Form w8a8_form(int M, int N, int K) {
@@ -449,10 +454,12 @@ W8A8Form w8a8_form(int M, int N, int K) {
     const struct {
       W8A8Form f;
       int mb, nb;
-    } small[] = {{kS4x2, 4, 2}, {kS2x4, 2, 4}, {kS2x2, 2, 2}, {kS2x1, 2, 1}, {kS1x2, 1, 2}, {kS1x1, 1, 1}};
+    } small[] = {{kS4x2, 4, 2}, {kS2x4, 2, 4}, {kS2x3, 2, 3}, {kS2x2, 2, 2}, {kS2x1, 2, 1}, {kS1x2, 1, 2}, {kS1x1, 1, 1}};
     for (const auto& s : small) {  // of equal ones the first: fewest reads of the weights
+      if (s.mb > 1 && M <= 8 * s.mb) continue;  // half the row blocks hold as many rows
       const double r = rounds(16 * s.mb, 16 * s.nb);
-      consider(s.f, 2.5 + r * (r >= 3 ? 1.2 : 1.0) * (s.mb + s.nb) * 16.0 * K / 45000.0);
+      const double rows = M < 16 * s.mb ? M : 16 * s.mb;
+      consider(s.f, 2.5 + r * (r >= 3 ? 1.2 : 1.0) * (rows + 16 * s.nb) * K / 45000.0);
     }
   }
   return best;
@@ -468,6 +475,7 @@ hipError_t launch_w8a8(const W8A8Args& a, hipStream_t stream) {
     case kS1x2: return a.M <= 8 ? launch_small<1, 2, 8, false>(a, stream) : launch_small<1, 2, 8, true>(a, stream);
     case kS2x1: return launch_small<2, 1, 16, true>(a, stream);
     case kS2x2: return launch_small<2, 2, 8, true>(a, stream);
+    case kS2x3: return launch_small<2, 3, 8, true>(a, stream);
     case kS4x2: return launch_small<4, 2, 8, true>(a, stream);
     case kS2x4: return launch_small<2, 4, 8, true>(a, stream);
     case kT64x64: return launch_tile<2, 2, 2, 2>(a, stream);
