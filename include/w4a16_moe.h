@@ -62,8 +62,8 @@ typedef struct w4a16_route_config {
 } w4a16_route_config;
 
 /* Workspace bytes of w4a16_moe_route for T tokens and E experts (0 for bad
- * arguments, and for the token counts that need none). 4-byte elements,
- * 16-byte aligned; its contents before and after a call do not matter. */
+ * arguments, and for the few tokens that need none). 16-byte aligned; its
+ * contents before and after a call do not matter. */
 size_t w4a16_moe_route_workspace_bytes(int T, int experts);
 
 /*
@@ -93,7 +93,7 @@ size_t w4a16_moe_route_workspace_bytes(int T, int experts);
  *             within an expert; -1 from offsets[E] on
  *   workspace : w4a16_moe_route_workspace_bytes(T, E) bytes (may be NULL if 0)
  * Every pointer 16-byte aligned (ids, weights, offsets, rows, bias: 4-byte).
- * T == 0 writes offsets (all 0) and nothing else. T * top_k <= 2^30.
+ * T == 0 writes offsets (all 0) and nothing else. T * top_k <= 2^26.
  * Returns W4A16_OK, W4A16_ERR_INVALID_ARG (bad field, null pointer, negative
  * size, workspace too small), W4A16_ERR_UNSUPPORTED (too many slots),
  * W4A16_ERR_MISALIGNED or W4A16_ERR_LAUNCH.
@@ -128,8 +128,8 @@ typedef enum {
  * a slot that is listed twice gives an unspecified one of its results.
  * Supported: 0 <= slots <= 2^30, 1 <= experts <= W4A16_ROUTE_MAX_EXPERTS,
  * x_div >= 1, N >= 1, group in {32, 64, 128, 256}, K % group == 0; SWIGLU needs
- * N % 32 == 0; x and one expert's packed weights below 4 GB each (else
- * W4A16_ERR_UNSUPPORTED). x, qweight, scales, y 16-byte aligned, the lists
+ * N % 32 == 0; x and one expert's packed weights below 4 GB each, and a grid
+ * of at most 2^32 threads (else W4A16_ERR_UNSUPPORTED). x, qweight, scales, y 16-byte aligned, the lists
  * 4-byte. slots == 0 launches nothing. y must not overlap any input.
  */
 int w4a16_gemm_experts(const void* x, const void* qweight, const void* scales, void* y,
@@ -178,8 +178,8 @@ int w8a8_pack(const int8_t* q, int8_t* qweight_out, int N, int K);
  *   qweight : device copy of what w8a8_pack wrote; sw : device f32 [N]
  *   y : device bf16 [M][N], overlapping no input
  * Supported: M >= 0, N >= 1, 16 <= K <= 131072 (so that no int32 sum can
- * overflow), K % 16 == 0, packed weights below 4 GB; other shapes return
- * W4A16_ERR_UNSUPPORTED. Every pointer 16-byte aligned (sw and sx: 4-byte).
+ * overflow), K % 16 == 0, packed weights below 4 GB, a grid of at most 2^32
+ * threads; other shapes return W4A16_ERR_UNSUPPORTED. Every pointer 16-byte aligned (sw and sx: 4-byte).
  * M == 0 launches nothing. Needs no workspace.
  */
 int w8a8_gemm(const void* xq, const float* sx, const void* qweight, const float* sw, void* y,

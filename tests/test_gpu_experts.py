@@ -147,6 +147,15 @@ def test_deep_products_of_few_rows(group, swiglu, T, N):
     check(10, N, 2560, group, ids, 8, swiglu, seed=T)
 
 
+@pytest.mark.parametrize("E,slots", [(300, 5), (300, 900), (1024, 40), (1024, 6000)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_many_experts(E, slots, swiglu):
+    """More experts than a lane holds offsets of in registers; most of them empty or small."""
+    rng = np.random.default_rng(E + slots)
+    ids = np.minimum((rng.random(slots) ** 2 * E).astype(int), E - 1)
+    check(E, 32, 64, 32, np.where(rng.random(slots) < 0.1, -1, ids), 1, swiglu, seed=slots)
+
+
 def test_one_expert_takes_all_and_others_none():
     for slots in (5, 100, 900):
         check(4, 64, 256, 128, np.full(slots, 2), 1, False)

@@ -146,16 +146,30 @@ def test_every_token_to_one_expert():
     check_route(z, None, 1)
 
 
-def test_no_tokens():
+@pytest.mark.parametrize("E", [8, 256, 257, 1024])
+def test_no_tokens(E):
     import torch
 
     import w4a16_weight_only_gemm_amd as w4
-    off = torch.full((9,), SENTINEL, dtype=torch.int32, device="cuda")
+    off = torch.full((E + 1,), SENTINEL, dtype=torch.int32, device="cuda")
     e = torch.empty(0, dtype=torch.int32, device="cuda")
     f = torch.empty(0, device="cuda")
-    w4.w4a16_moe_route(torch.empty(0, 8, device="cuda"), None, 0, 8, 2, e, f, off, e, None)
+    n = w4.w4a16_moe_route_workspace_bytes(0, E)
+    ws = torch.zeros(n // 4, dtype=torch.int32, device="cuda") if n else None
+    w4.w4a16_moe_route(torch.empty(0, E, device="cuda"), None, 0, E, 2, e, f, off, e, ws)
     torch.cuda.synchronize()
-    assert off.tolist() == [0] * 9
+    assert off.tolist() == [0] * (E + 1)
+
+
+@pytest.mark.parametrize("E,T", [(300, 40), (700, 7), (1024, 1500), (257, 9000)])
+def test_many_experts(E, T):
+    """More experts than one launch and four per lane hold, with few and many tokens."""
+    rng = np.random.default_rng(E)
+    z = rng.standard_normal((T, E)).astype(np.float32)
+    check_route(z, None, 4)
+    if T < 2000:
+        check_route(z, rng.standard_normal(E) * 0.1, 8, scoring="sigmoid", groups=E // 10 if E == 300 else 4
+                    if E % 4 == 0 else 1, groups_kept=2 if E % 4 == 0 else 1, group_top=2)
 
 
 def test_repeated_calls_give_the_same_bits():

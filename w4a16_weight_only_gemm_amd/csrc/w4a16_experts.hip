@@ -353,11 +353,11 @@ hipError_t launch_small_t(const ExpertsArgs& a, hipStream_t stream) {
   int NT = ACT ? (NCB / 2 + NB / 2 - 1) / (NB / 2) : (NCB + NB - 1) / NB;
   const long long row_tiles = a.slots / TM + (a.slots < a.E ? a.slots : a.E);
   const long long blocks = row_tiles * NT;
-  if (blocks * 64 * WAVES > 0xFFFFFFFFLL) return hipErrorInvalidValue;
+  if (blocks * 64 * WAVES > 0xFFFFFFFFLL) return hipErrorNotSupported;
   size_t lds = static_cast<size_t>(WAVES) * MB * NB * 1024;
   if (XS) lds += static_cast<size_t>(WAVES) * MB * 16 * 256;
   const void* fn = reinterpret_cast<const void*>(&experts_small_kernel<GS, MB, NB, WAVES, P4, P16, XS, ACT>);
-  if (lds > 64 * 1024) {
+  if (lds >= 64 * 1024) {
     const hipError_t e =
         hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
     if (e != hipSuccess) return e;
@@ -484,7 +484,7 @@ hipError_t launch_tile_t(const ExpertsArgs& a, hipStream_t stream) {
   int NT = ACT ? (NCB / 2 + kLgWaves - 1) / kLgWaves : (NCB + kLgBlocks - 1) / kLgBlocks;
   const long long row_tiles = a.slots / Rows + (a.slots < a.E ? a.slots : a.E);
   const long long blocks = row_tiles * NT;
-  if (blocks * kLgThreads > 0xFFFFFFFFLL) return hipErrorInvalidValue;
+  if (blocks * kLgThreads > 0xFFFFFFFFLL) return hipErrorNotSupported;
   const void* fn = reinterpret_cast<const void*>(&experts_tile_kernel<GS, MB, ACT>);
   if (Lds > 64 * 1024) {
     const hipError_t e =

@@ -547,7 +547,8 @@ int experts_per_lane(int E) {
 bool route_one(int T, int E) { return T <= kRtOneLaunchTokens && E <= kRtOneLaunchExperts; }
 int route_chunk(int T) { return T <= kRtFewTokens ? kRtFewChunk : T <= kRtMidTokens ? kRtMidChunk : kRtChunk; }
 int route_chunks(int T) {
-  return static_cast<int>((static_cast<long long>(T) + route_chunk(T) - 1) / route_chunk(T));
+  const long long n = (static_cast<long long>(T) + route_chunk(T) - 1) / route_chunk(T);
+  return n > 0 ? static_cast<int>(n) : 1;  // no tokens: one workgroup writes the offsets
 }
 // Workspace: the chunks' counts, then (many chunks) their running sums.
 size_t counts_bytes(int T, int E) {
@@ -653,7 +654,7 @@ size_t route_workspace_bytes(int T, int E) {
 
 hipError_t launch_route(RouteArgs a, hipStream_t stream) {
   a.chunk = route_one(a.T, a.E) ? kRtOneLaunchTokens : route_chunk(a.T);
-  a.chunks = route_one(a.T, a.E) || a.T == 0 ? 1 : route_chunks(a.T);
+  a.chunks = route_one(a.T, a.E) ? 1 : route_chunks(a.T);
   a.per = a.E / a.groups;
   a.per_inverse = static_cast<uint32_t>(0xFFFFFFFFu / a.per + 1);  // not used for one expert per group (then whole)
   const int held = experts_per_lane(a.E);

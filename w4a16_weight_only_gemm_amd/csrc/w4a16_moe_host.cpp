@@ -11,11 +11,16 @@
 namespace {
 
 constexpr long long kMaxSlots = 1LL << 30;
+constexpr long long kMaxRoutedSlots = 1LL << 26;
 constexpr long long kMaxBuffer = 0xFFFFFE00LL;  // bytes a 32-bit buffer resource may span
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-int status(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_LAUNCH; }
+// The launchers return hipErrorNotSupported, before any launch, for a grid of
+// more than 2^32 threads.
+int status(hipError_t e) {
+  return e == hipSuccess ? W4A16_OK : e == hipErrorNotSupported ? W4A16_ERR_UNSUPPORTED : W4A16_ERR_LAUNCH;
+}
 
 // byte j of a 16-block holds the code of offset kOrder[j] (as w4a8_quantize)
 constexpr int kOrder[16] = {0, 4, 1, 5, 2, 6, 3, 7, 8, 12, 9, 13, 10, 14, 11, 15};
@@ -47,7 +52,7 @@ int w4a16_moe_route(const void* logits, const float* bias, const w4a16_route_con
   if (!std::isfinite(c->scale)) return W4A16_ERR_INVALID_ARG;
   if (!offsets) return W4A16_ERR_INVALID_ARG;
   if (T > 0 && (!logits || !ids || !weights || !rows)) return W4A16_ERR_INVALID_ARG;
-  if (static_cast<long long>(T) * c->top_k > kMaxSlots) return W4A16_ERR_UNSUPPORTED;
+  if (static_cast<long long>(T) * c->top_k > kMaxRoutedSlots) return W4A16_ERR_UNSUPPORTED;
   const size_t need = w4a16_internal::route_workspace_bytes(T, c->experts);
   if (need > 0 && (!workspace || workspace_bytes < need)) return W4A16_ERR_INVALID_ARG;
   if (!aligned(logits, 16) || !aligned(workspace, 16) || !aligned(bias, 4) || !aligned(ids, 4) ||

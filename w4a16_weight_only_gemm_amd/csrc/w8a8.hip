@@ -166,7 +166,7 @@ hipError_t launch_small(const W8A8Args& a, hipStream_t stream) {
   const int NCB = (a.N + 15) / 16;
   const size_t lds = static_cast<size_t>(WAVES) * MB * 1024 * (XS && NB < 2 ? 2 : NB);
   const void* fn = reinterpret_cast<const void*>(&w8a8_small_kernel<MB, NB, WAVES, XS>);
-  if (lds > 64 * 1024) {
+  if (lds >= 64 * 1024) {
     const hipError_t e =
         hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
     if (e != hipSuccess) return e;
@@ -405,7 +405,7 @@ hipError_t launch_tile(const W8A8Args& a, hipStream_t stream) {
   int MT = static_cast<int>((static_cast<long long>(a.M) + C::Rows - 1) / C::Rows);
   int NT = (NCB + C::Blocks - 1) / C::Blocks;
   const long long blocks = static_cast<long long>(MT) * NT;
-  if (blocks * C::Threads > 0xFFFFFFFFLL) return hipErrorInvalidValue;
+  if (blocks * C::Threads > 0xFFFFFFFFLL) return hipErrorNotSupported;
   const void* fn = reinterpret_cast<const void*>(&w8a8_tile_kernel<WM, WN, MB, NB>);
   if (C::Lds > 64 * 1024) {
     const hipError_t e =
