@@ -62,8 +62,9 @@ typedef struct w4a16_route_config {
 } w4a16_route_config;
 
 /* Workspace bytes of w4a16_moe_route for T tokens and E experts (0 for bad
- * arguments, and for the few tokens that need none). 16-byte aligned; its
- * contents before and after a call do not matter. */
+ * arguments, and for the few tokens that need none): enough for fewer tokens or
+ * experts too. 16-byte aligned; its contents before and after a call do not
+ * matter. */
 size_t w4a16_moe_route_workspace_bytes(int T, int experts);
 
 /*

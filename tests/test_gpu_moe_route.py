@@ -258,3 +258,31 @@ def test_large_biases(bias):
     b = np.where(rng.random(64) < 0.4, bias, 0.1)
     check_route(rng.standard_normal((50, 64)).astype(np.float32), b, 6, scoring="sigmoid")
     check_route(rng.standard_normal((50, 64)).astype(np.float32) * 60, b, 6, groups=4, groups_kept=2)
+
+
+@pytest.mark.parametrize("E", [40, 128, 256, 500, 1000])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_logits_next_to_each_other(E, bf16):
+    """Neighbouring logits, in every order within and across lanes: 0 to 15 steps
+    of fp32 apart (bf16: of bf16), some of them equal."""
+    rng = np.random.default_rng(E)
+    base = np.float32([3.0, -3.0, 1e-3, 0.0, 100.0] * 12)[:, None]
+    steps = rng.integers(0, 16, (60, E)).astype(np.int64)
+    bits = np.repeat(base, E, 1).view(np.int32).astype(np.int64) + steps * (65536 if bf16 else 1)
+    z = bits.astype(np.int32).view(np.float32)
+    z[1::2, 5:] -= 50.0  # few of them alone at the top
+    check_route(z, None, 8, bf16=bf16)
+    check_route(z, None, 5, bf16=bf16, renormalize=False)
+    check_route(z, None, 3, bf16=bf16, scoring="sigmoid", groups=4, groups_kept=2, group_top=2)
+
+
+@pytest.mark.parametrize("E,groups", [(72, 8), (256, 8), (1024, 16)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_many_equal_values(E, groups, scoring):
+    """More equal values than a wave has lanes, beside distinct ones."""
+    rng = np.random.default_rng(E)
+    z = np.where(rng.random((40, E)) < 0.9, 0.5, rng.standard_normal((40, E)) * 2).astype(np.float32)
+    z[0] = 0.5
+    for b in (None, np.full(E, 0.25)):
+        check_route(z, b, 8, scoring=scoring)
+        check_route(z, b, 8, scoring=scoring, groups=groups, groups_kept=3, group_top=2)

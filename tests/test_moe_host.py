@@ -109,6 +109,13 @@ def test_route_refusals():
     assert w4.w4a16_moe_route_workspace_bytes(-1, 64) == 0
     assert w4.w4a16_moe_route_workspace_bytes(1000, 0) == 0
     assert w4.w4a16_moe_route_workspace_bytes(1000, 1025) == 0
+    for E in (1, 8, 200, 256, 257, 1024):  # a workspace for the most tokens serves fewer
+        sizes = [w4.w4a16_moe_route_workspace_bytes(T, E)
+                 for T in (*range(0, 40), 1000, 1024, 1025, 4096, 4097, 8192, 8193, 100000)]
+        assert sizes == sorted(sizes), E
+    for T in (0, 17, 1025, 9000):
+        sizes = [w4.w4a16_moe_route_workspace_bytes(T, E) for E in range(1, 1025)]
+        assert sizes == sorted(sizes), T
 
 
 def test_experts_refusals():

@@ -1,23 +1,30 @@
 // w4a16_moe.hip -- routing of tokens to experts, and the weighted sum of the
 // experts' rows back into token order.
 //
-// Routing (w4a16_moe_route). One wave per token: lane l holds the P experts l P
-// .. l P + P - 1. Each expert gets an integer key whose order is the order of
-// choice; top_k rounds of a wave-wide maximum (DPP, no LDS) take the choices,
-// and a ballot finds the first lane that holds it: the lowest index of equal
-// ones.
+// Routing (w4a16_moe_route). One wave per token, each lane holding P experts.
+// An expert gets an integer key whose order is the order of choice, with the
+// expert's place in its lane in the lowest bits. A lane sorts its keys once;
+// each choice is then one maximum over the lanes' first keys (six DPP steps, no
+// LDS), the lane that holds it moving up by one. Keys too near to tell are
+// sorted out afterwards, and only among the choices and those next to them:
 //  * Without bias and groups the choice is by score, which grows with the
-//    logit: the key is the logit's own bits, order-preserving. No arithmetic,
-//    so nothing can round.
+//    logit: the key is the logit's own bits, order-preserving. bf16 keys are
+//    exact; fp32 logits whose keys differ in the lowest bits only are compared
+//    again as they are.
 //  * With a bias or groups the choice values are what the interface defines in
 //    64 bits: in fp32 two experts a few 1e-8 apart could swap places. They are
-//    first formed in fp32; where a decision (a choice against the next one, a
-//    group against another) is nearer than a margin that covers every fp32
-//    rounding on the way, the token is decided again in fp64. That is one token
-//    of some hundreds with a router of 256 experts, and every exact tie.
-// The weights need the scores of the chosen experts only, in fp64: lane j
-// computes the j-th choice's (softmax without renormalisation also sums over
-// all experts, in fp64).
+//    first formed in fp32; choices nearer than a margin that covers every fp32
+//    rounding on the way are formed in fp64, a lane each, and ordered by that. Of
+//    groups only the last one kept and the first one dropped have to be apart;
+//    where they are not, the token's groups are formed again in fp64. Either
+//    happens to one token of some hundreds with a router of 256 experts.
+// The weights need the scores of the chosen experts only, in fp64: a thread per
+// slot, after the workgroup's tokens are chosen (softmax without renormalisation
+// also sums over all experts, in fp64).
+// What bounds it: few tokens, the launches and the chain of dependent steps;
+// many, the vector instructions of the rounds (8192 tokens of 256 experts, 8
+// each, in groups: 14 us of 21; 6.9 us are the second launch). Choosing from
+// unsorted keys with every near token decided again in fp64 took 23 us there.
 //
 // Lists. Slots are ordered by expert and ascending within one, so the result
 // does not depend on timing: a workgroup owns a chunk of consecutive tokens,
@@ -42,16 +49,17 @@ constexpr int kRtThreads = 1024;
 constexpr int kRtWaves = kRtThreads / 64;
 constexpr int kRtMaxExperts = 1024;
 // Tokens per workgroup (a wave takes one after the other), by the number of
-// tokens. A token takes a wave some 3 to 8 us of dependent steps, so few tokens
+// tokens. A token takes a wave some 2 to 4 us of dependent steps, so few tokens
 // are spread over many workgroups; the second launch reads every chunk's
 // counts in every workgroup, so many tokens are not. Measured at 256 experts,
 // 8 per token (us, plain top-k / bias and groups):
-//   1 token: one workgroup and launch 5.1 / 7.9
-//   16 tokens: one workgroup and launch 8.2 / 12.3, 4 per workgroup and two
-//     launches 8.6 / 11.3
-//   64 tokens: 16 per workgroup 11.3 / 18.8, 4 per workgroup 9.2 / 15.9
-//   4096 tokens: 16 per workgroup 14.3 / 22.1, 32 per workgroup 18.3 / 29.1
-constexpr int kRtOneLaunchTokens = 8;   // one launch up to here, and up to
+//   1 token: one workgroup and launch 5.3 / 6.7
+//   16 tokens: one workgroup and launch 7.0 / 9.6, 4 per workgroup and two
+//     launches 8.5 / 9.8
+//   64 tokens: 16 per workgroup 9.8 / 12.3, 4 per workgroup 8.9 / 10.1
+//   2048 tokens: 4 per workgroup 15.0 / 17.3, 16 per workgroup 12.4 / 15.2
+//   4096 tokens: 16 per workgroup 11.8 / 15.6, 32 per workgroup 16.0 / 21.4
+constexpr int kRtOneLaunchTokens = 16;  // one launch up to here, and up to
 constexpr int kRtOneLaunchExperts = 256;
 constexpr int kRtFewTokens = 1024;      // up to here 4 tokens and 4 waves
 constexpr int kRtFewChunk = 4;
@@ -71,24 +79,26 @@ __device__ __forceinline__ uint64_t order_key(double f) {
   return b >> 63 ? ~b : b | 0x8000000000000000ull;
 }
 
-// The number an fp32 key stands for.
+// The number a key stands for.
 __device__ __forceinline__ float value_of(uint32_t k) {
   return __builtin_bit_cast(float, k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
+__device__ __forceinline__ double value_of(uint64_t k) {
+  return __builtin_bit_cast(double, k >> 63 ? k & 0x7FFFFFFFFFFFFFFFull : ~k);
+}
 
-// v of another lane: CTRL as in dpp_f32, for any 4- or 8-byte type; lanes that
-// the pattern does not reach (ROWS: the rows written) keep v.
+// v of another lane: CTRL as in dpp_f32, for any 4- or 8-byte type; 0 where the
+// pattern does not reach (ROWS: the rows written).
 template <int CTRL, int ROWS, typename T>
 __device__ __forceinline__ T dpp_of(T v) {
   if constexpr (sizeof(T) == 4) {
     const int b = __builtin_bit_cast(int, v);
-    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(b, b, CTRL, ROWS, 0xF, false));
+    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, b, CTRL, ROWS, 0xF, false));
   } else {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const int lo = static_cast<int>(b), hi = static_cast<int>(b >> 32);
-    const uint32_t nlo = __builtin_amdgcn_update_dpp(lo, lo, CTRL, ROWS, 0xF, false);
-    const uint32_t nhi = __builtin_amdgcn_update_dpp(hi, hi, CTRL, ROWS, 0xF, false);
-    return __builtin_bit_cast(T, static_cast<uint64_t>(nhi) << 32 | nlo);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, ROWS, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROWS, 0xF, false);
+    return __builtin_bit_cast(T, static_cast<uint64_t>(hi) << 32 | lo);
   }
 }
 
@@ -106,8 +116,8 @@ __device__ __forceinline__ T lane_of(T v, int src) {
 }
 
 // Maximum over the wave, in every lane: within quads, half rows and rows of 16
-// lanes, then from row to row into lane 63. Lanes a step does not reach meet
-// their own value.
+// lanes, then from row to row into lane 63. A lane a step does not reach meets
+// 0, so keys only.
 template <typename T>
 __device__ __forceinline__ T wave_max_of(T v) {
   auto step = [](T a, T b) { return b > a ? b : a; };
@@ -169,24 +179,29 @@ __device__ __forceinline__ S reciprocal(S x) {
     return 1.0 / x;
 }
 
-// What a wave knows of a token: the logits of its lane's experts, which of
-// them can be chosen, and the largest.
+// What a wave knows of a token: the logits of its lane's experts, and which of
+// them can be chosen.
 template <int P>
 struct Token {
+  size_t row;  // of its first logit
   float z[P];
   bool live[P];
-  float zmax;
 };
 
-// The top_k largest keys (0: never), one after the other: lane j gets the j-th
-// choice (-1 where nothing is left) and its logit. seen(j, key) is called for
-// every choice and once more for the best that was left.
-template <int P, typename Key, typename F>
-__device__ __forceinline__ void take(Key (&key)[P], const Token<P>& tk, int top_k, int lane, int& id,
-                                     float& logit, F seen) {
-  id = -1;
-  logit = 0.f;
-  for (int j = 0;; ++j) {
+// The i-th expert of a lane. Choice by value takes consecutive ones, so that
+// groups are whole lanes; choice by logit takes every 64th, so that the order
+// of (i, lane) is that of the experts and equal keys need no second look.
+template <int P, bool WIDE>
+__device__ __forceinline__ int expert_of(int lane, int i) {
+  return WIDE ? lane * P + i : i * 64 + lane;
+}
+
+// The top_k largest keys (0: never), one after the other, the lowest expert of
+// equal ones first: lane j gets the j-th choice, -1 where nothing is left.
+template <int P, bool WIDE, typename Key>
+__device__ __forceinline__ int take(Key (&key)[P], int top_k, int lane) {
+  int id = -1;
+  for (int j = 0; j < top_k; ++j) {
     Key best = key[0];
     int bi = 0;
 #pragma unroll
@@ -197,171 +212,324 @@ __device__ __forceinline__ void take(Key (&key)[P], const Token<P>& tk, int top_
       }
     const Key top = wave_max_of(best);
     if (top == 0) break;
-    if (!seen(j, top) || j == top_k) break;
-    const int owner = __builtin_ctzll(__ballot(best == top));
-    float bz = tk.z[0];
+    const uint32_t back = best == top ? kRtMaxExperts - expert_of<P, WIDE>(lane, bi) : 0;
+    const int e = kRtMaxExperts - static_cast<int>(wave_max_of(back));
+    if (lane == j) id = e;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      if (i > 0 && bi == i) bz = tk.z[i];
-      if (bi == i && lane == owner) key[i] = 0;
-    }
-    const int e = owner * P + __builtin_amdgcn_readlane(bi, owner);
-    const float ez = lane_of(bz, owner);
+    for (int i = 0; i < P; ++i)
+      if (expert_of<P, WIDE>(lane, i) == e) key[i] = 0;
+  }
+  return id;
+}
+
+// The same from 32-bit keys whose low bits (P - 1, a mask) give way to P - 1 -
+// i, so that a key names its expert within the lane: a lane's keys are sorted
+// once by plain maxima and minima, and a round is one maximum over the lanes'
+// first keys, after which the lane that held it moves its keys up.
+// Keys that are not apart may be in the wrong order: past top_k the rounds go on
+// until one is apart from the key before it. Lane j < the number returned gets
+// the j-th key in rank and its expert in id; 65 says that 64 were not enough.
+template <int P, bool WIDE, typename F>
+__device__ __forceinline__ int take_packed(uint32_t (&key)[P], int top_k, int lane, uint32_t& rank,
+                                           int& id, F apart) {
+  // odd-even merge sort, descending
+#pragma unroll
+  for (int p = 1; p < P; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < P; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < P && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t x = key[i + j], y = key[i + j + k];
+            key[i + j] = x > y ? x : y;
+            key[i + j + k] = x > y ? y : x;
+          }
+  id = -1;
+  rank = 0;
+  uint32_t last = 0;
+  auto accept = [&](int j, uint32_t top) {
+    const int owner = __builtin_ctzll(__ballot(key[0] == top));
+    const int e = expert_of<P, WIDE>(owner, P - 1 - static_cast<int>(top & (P - 1)));
     if (lane == j) {
+      rank = top;
       id = e;
-      logit = ez;
     }
+    last = top;
+    const uint32_t mine = lane == owner ? ~0u : 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) key[i] = (key[i] & ~mine) | ((i + 1 < P ? key[i + 1] : 0) & mine);
+  };
+  int j = 0;
+  for (; j < top_k; ++j) {
+    const uint32_t top = wave_max_of(key[0]);
+    if (top == 0) return j;
+    accept(j, top);
+  }
+  for (;; ++j) {
+    const uint32_t top = wave_max_of(key[0]);
+    if (top == 0 || apart(last, top)) return j;
+    if (j == 64) return 65;
+    accept(j, top);
   }
 }
 
-// Choice by values (bias or groups) in S. Returns whether every decision is
-// further than the margin (S = double: always). vals: the wave's LDS.
-template <int P, typename S>
-__device__ __forceinline__ bool choose_by_value(const RouteArgs& a, const Token<P>& tk, int lane,
-                                                S* vals, int& id, float& logit) {
-  constexpr bool kCheck = sizeof(S) == 4;
-  bool sure = true;
-  S margin = kRtMarginSigmoid;
-  auto apart = [&](S hi, S lo) {
-    if constexpr (!kCheck) return true;
-    const S m = hi > -lo ? hi : -lo;  // the larger magnitude, as hi >= lo
-    return hi - lo > margin + kRtMarginValue * m;
+// Lanes 0 .. n - 1 hold different experts and their values: puts the experts in
+// order of value, the lowest first among equal ones.
+template <typename S>
+__device__ __forceinline__ int in_order(int id, S value, int n, int lane) {
+  int place = 0;
+  for (int q = 0; q < n; ++q) {
+    const S ov = lane_of(value, q);
+    const int oe = __builtin_amdgcn_readlane(id, q);
+    place += ov > value || (ov == value && oe < id);
+  }
+  return __builtin_amdgcn_ds_permute(4 * (lane < n ? place : lane), id);
+}
+
+// Largest logit of the token.
+template <int P>
+__device__ __forceinline__ float largest(const Token<P>& tk) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const uint32_t k = tk.live[i] ? order_key(tk.z[i]) : 0;
+    m = k > m ? k : m;
+  }
+  m = wave_max_of(m);
+  return m ? value_of(m) : 0.f;
+}
+
+// The two largest of the lanes' keys (t1 >= t2) within runs of lg lanes, lg a power
+// of two, in every lane of the run.
+template <typename Key>
+__device__ __forceinline__ void merge_pairs(Key& t1, Key& t2, int lg) {
+  auto merge = [&](Key o1, Key o2) {
+    const Key lo = t1 < o1 ? t1 : o1, hi2 = t2 > o2 ? t2 : o2;
+    t1 = t1 > o1 ? t1 : o1;
+    t2 = lo > hi2 ? lo : hi2;
   };
+  // after a step all lanes of a run of that length hold the same, so a mirror
+  // within twice the length reaches the other run
+  if (lg >= 2) merge(dpp_of<0xB1, 0xF>(t1), dpp_of<0xB1, 0xF>(t2));
+  if (lg >= 4) merge(dpp_of<0x4E, 0xF>(t1), dpp_of<0x4E, 0xF>(t2));
+  if (lg >= 8) merge(dpp_of<0x141, 0xF>(t1), dpp_of<0x141, 0xF>(t2));
+  if (lg >= 16) merge(dpp_of<0x140, 0xF>(t1), dpp_of<0x140, 0xF>(t2));
+  for (int o = 16; o < lg; o <<= 1) {
+    merge(__shfl_xor(t1, o), __shfl_xor(t2, o));
+  }
+}
+
+// The choice values of the lane's experts in S, as keys (0 where not live), and
+// for S = float the margin. sum: the softmax's.
+template <int P, typename S, typename Key>
+__device__ __forceinline__ void choice_keys(const RouteArgs& a, const Token<P>& tk, float zmax,
+                                            int lane, Key (&key)[P], S& sum, float& margin) {
   S v[P];
-  S part = 0;
+  sum = 0;
+  if (a.sigmoid) {
+    margin = kRtMarginSigmoid;
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const S x = tk.z[i];
-    v[i] = 0;
-    if (tk.live[i]) v[i] = a.sigmoid ? reciprocal<S>(1 + exp_of<S>(-x)) : exp_of<S>(x - static_cast<S>(tk.zmax));
-    part += v[i];
-  }
-  if (!a.sigmoid) {
-    const S sum = wave_sum_of(part);  // 0: nothing is live
-    margin = kRtMarginSoftmax / sum;  // the largest score is 1 / sum
+    for (int i = 0; i < P; ++i) v[i] = reciprocal<S>(1 + exp_of<S>(-static_cast<S>(tk.z[i])));
+  } else {
 #pragma unroll
-    for (int i = 0; i < P; ++i) v[i] = tk.live[i] ? v[i] / sum : 0;
-  }
+    for (int i = 0; i < P; ++i) {
+      v[i] = exp_of<S>(static_cast<S>(tk.z[i]) - static_cast<S>(zmax));
+      sum += tk.live[i] ? v[i] : 0;
+    }
+    sum = wave_sum_of(sum);  // 0: nothing is live
+    margin = kRtMarginSoftmax / static_cast<float>(sum);  // the largest score is 1 / sum
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int e = lane * P + i;
-    if (a.bias && e < a.E) v[i] += static_cast<S>(a.bias[e]);
+    for (int i = 0; i < P; ++i) v[i] = sizeof(S) == 4 ? v[i] * reciprocal<S>(sum) : v[i] / sum;
   }
-  typename std::conditional<kCheck, uint32_t, uint64_t>::type key[P];
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      v[i] += static_cast<S>(a.bias[min(expert_of<P, true>(lane, i), a.E - 1)]);
+  }
 #pragma unroll
   for (int i = 0; i < P; ++i) key[i] = tk.live[i] ? order_key(v[i]) : 0;
-  if (a.groups > 1) {
-    // a group's two largest values, by lg lanes (a power of two) each
-    const S none = -static_cast<S>(__builtin_inff());
-    S t1 = none, t2 = none;
-    auto put = [&](S x) {
-      t2 = x > t1 ? t1 : x > t2 ? x : t2;
-      t1 = x > t1 ? x : t1;
-    };
-    const int per = a.per, lg = a.group_lanes, g = lane / lg;
-    if (a.group_whole) {  // the lanes that hold the group's experts
-#pragma unroll
-      for (int i = 0; i < P; ++i) put(tk.live[i] ? v[i] : none);
-    } else {
-#pragma unroll
-      for (int i = 0; i < P; ++i)
-        if (lane * P + i < a.E) vals[lane * P + i] = tk.live[i] ? v[i] : none;
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      if (g < a.groups)
-        for (int j = lane % lg; j < per; j += lg) put(vals[g * per + j]);
-    }
-    for (int o = 1; o < lg; o <<= 1) {
-      const S o1 = __shfl_xor(t1, o), o2 = __shfl_xor(t2, o);
-      const S lo = t1 < o1 ? t1 : o1, hi2 = t2 > o2 ? t2 : o2;
-      t1 = t1 > o1 ? t1 : o1;
-      t2 = lo > hi2 ? lo : hi2;
-    }
-    S value = t1;
-    if (a.group_top == 2 && t2 > none) value = t1 + t2;
-    int rank = 0;
-    bool near = false;
-    for (int q = 0; q < a.groups; ++q) {
-      const S ov = lane_of(value, q * lg);
-      if (ov > value || (ov == value && q < g)) ++rank;
-      if (kCheck && q != g && value > none && ov > none)
-        near |= !(ov > value ? apart(ov, value) : apart(value, ov));
-    }
-    sure = !__any(g < a.groups && near);
-    const uint64_t kept = __ballot(g < a.groups && rank < a.groups_kept);
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int e = lane * P + i;
-      const int eg = a.group_whole ? g : static_cast<int>(__umulhi(e, a.per_inverse));  // e / per
-      if (e < a.E && !((kept >> (eg * lg)) & 1)) key[i] = 0;
-    }
-  }
-  if (!sure) return false;
-  S last = 0;
-  take<P>(key, tk, a.top_k, lane, id, logit, [&](int j, auto k) {
-    if constexpr (kCheck) {
-      const S x = value_of(k);
-      if (j > 0 && !apart(last, x)) sure = false;
-      last = x;
-      return sure;
-    } else {
-      return j < a.top_k;
-    }
-  });
-  return sure;
 }
 
-// The choices of token t, by one wave. P: experts per lane. WIDE: bias or
-// groups. vals: this wave's LDS for E choice values (WIDE). Lane j < top_k
-// returns the j-th choice (or -1) in id and its weight.
-template <int P, bool WIDE>
-__device__ __forceinline__ void choose(const RouteArgs& a, int t, int lane, double* vals, int& id,
-                                       float& weight) {
-  const size_t row = static_cast<size_t>(t) * a.E;
-  Token<P> tk;
+// Whether fp32 values hi >= lo are further apart than their errors.
+__device__ __forceinline__ bool apart_by(float hi, float lo, float margin, float relative) {
+  const float m = hi > -lo ? hi : -lo;  // the larger magnitude
+  return hi - lo > margin + relative * m;
+}
+
+// keep: a bit per expert of the lane, whether its group is kept. Returns false,
+// and no bits, where the last group kept is nearer than the margin to the first
+// one dropped (S = float). vals: the wave's LDS.
+template <int P, typename S, typename Key>
+__device__ __forceinline__ bool keep_groups(const RouteArgs& a, Key (&key)[P], float margin, int lane,
+                                            Key* vals, uint32_t& keep) {
+  // a group's two largest values, by lg lanes (a power of two) each
+  Key t1 = 0, t2 = 0;
+  auto put = [&](Key x) {
+    const Key lo = x < t1 ? x : t1;
+    t2 = t2 > lo ? t2 : lo;
+    t1 = x > t1 ? x : t1;
+  };
+  const int per = a.per, lg = a.group_lanes, g = lane / lg;
+  if (a.group_whole) {  // the lanes that hold the group's experts
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int e = lane * P + i;
-    tk.z[i] = e < a.E ? load_logit(a, row + e) : -__builtin_inff();
-  }
-#pragma unroll
-  for (int i = 0; i < P; ++i) tk.live[i] = live_logit(tk.z[i]);
-  tk.zmax = -FLT_MAX;
-  if (!a.sigmoid) {
-#pragma unroll
-    for (int i = 0; i < P; ++i) tk.zmax = tk.live[i] && tk.z[i] > tk.zmax ? tk.z[i] : tk.zmax;
-    tk.zmax = wave_max_of(tk.zmax);
-  }
-  float logit;
-  if constexpr (WIDE) {
-    if (!choose_by_value<P, float>(a, tk, lane, reinterpret_cast<float*>(vals), id, logit))
-      choose_by_value<P, double>(a, tk, lane, vals, id, logit);
+    for (int i = 0; i < P; ++i) put(key[i]);
   } else {
-    uint32_t key[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) key[i] = tk.live[i] ? order_key(tk.z[i]) : 0;
-    take<P>(key, tk, a.top_k, lane, id, logit, [&](int j, uint32_t) { return j < a.top_k; });
+    for (int i = 0; i < P; ++i)
+      if (lane * P + i < a.E) vals[lane * P + i] = key[i];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    if (g < a.groups)
+      for (int j = lane % lg; j < per; j += lg) put(vals[g * per + j]);
   }
-  double s = 0.0;
-  if (id >= 0)
-    s = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(logit)))
-                  : exp(static_cast<double>(logit) - tk.zmax);
-  double total = 1.0;
-  if (a.renormalize) {  // the softmax's own sum cancels
-    total = wave_sum_of(s);
-  } else if (!a.sigmoid) {
+  merge_pairs(t1, t2, lg);
+  const S none = -static_cast<S>(__builtin_inff());
+  S value = t1 ? value_of(t1) : none;
+  if (a.group_top == 2 && t2) value += value_of(t2);
+  // the groups with a larger value, or an equal one and a lower index
+  int place = g < a.groups ? 0 : a.groups;
+  for (int q = 0; q < a.groups; ++q) {
+    const S ov = lane_of(value, q * lg);
+    place += ov > value || (ov == value && g > q);
+  }
+  if (sizeof(S) == 4 && a.groups_kept < a.groups) {
+    const S low = lane_of(value, __builtin_ctzll(__ballot(place == a.groups_kept - 1)));
+    const S high = lane_of(value, __builtin_ctzll(__ballot(place == a.groups_kept)));
+    if (high > none && !apart_by(low, high, margin, kRtMarginValue)) return false;
+  }
+  const bool in = place < a.groups_kept;
+  if (a.group_whole) {
+    keep = in ? ~0u : 0;
+  } else {
+    const uint64_t kept = __ballot(in);
+    keep = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int eg = static_cast<int>(__umulhi(lane * P + i, a.per_inverse));  // e / per
+      keep |= static_cast<uint32_t>(kept >> (eg * lg & 63) & 1) << i;
+    }
+  }
+  return true;
+}
+
+// Choice by values (bias or groups): lane j < top_k gets the j-th choice.
+// Decisions in fp32, those nearer than the margin again in fp64. vals: the
+// wave's LDS.
+template <int P>
+__device__ __forceinline__ int choose_by_value(const RouteArgs& a, const Token<P>& tk, float zmax,
+                                               int lane, double* vals) {
+  uint32_t key[P], rank, keep = ~0u;
+  uint64_t wide[P];
+  float sum, margin, unused;
+  double wsum = 1.0;
+  choice_keys<P>(a, tk, zmax, lane, key, sum, margin);
+  if (a.groups > 1 &&
+      !keep_groups<P, float>(a, key, margin, lane, reinterpret_cast<uint32_t*>(vals), keep)) {
+    choice_keys<P>(a, tk, zmax, lane, wide, wsum, unused);
+    keep_groups<P, double>(a, wide, 0.f, lane, reinterpret_cast<uint64_t*>(vals), keep);
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    key[i] = (keep >> i & 1) && key[i] ? (key[i] & ~static_cast<uint32_t>(P - 1)) | (P - 1 - i) : 0;
+  // dropped key bits are at most P - 1 units of 2^-23 of the value
+  auto apart = [&](uint32_t hi, uint32_t lo) {
+    return apart_by(value_of(hi & ~(P - 1u)), value_of(lo & ~(P - 1u)), margin,
+                    kRtMarginValue + P * 0x1p-23f);
+  };
+  int id;
+  const int n = take_packed<P, true>(key, a.top_k, lane, rank, id, apart);
+  const uint32_t before = __shfl_up(rank, 1);
+  const bool near = lane > 0 && lane < n && !apart(before, rank);
+  if (!__any(near)) return id;
+  if (n > 64 || !a.sigmoid) choice_keys<P>(a, tk, zmax, lane, wide, wsum, unused);
+  if (n > 64) {
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (!(keep >> i & 1)) wide[i] = 0;
+    return take<P, true>(wide, a.top_k, lane);
+  }
+  // the candidates' own values
+  double x = 0.0;
+  if (id >= 0) {
+    float z = load_logit(a, tk.row + id);
+    live_logit(z);
+    x = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(z)))
+                  : exp(static_cast<double>(z) - static_cast<double>(zmax)) / wsum;
+    if (a.bias) x += static_cast<double>(a.bias[id]);
+  }
+  return in_order(id, x, n, lane);
+}
+
+// The choices of token t, by one wave: lane j < top_k gets the j-th, or -1.
+// P: experts per lane. WIDE: bias or groups. vals: this wave's LDS for E choice
+// values (WIDE). zmax: the largest logit, for a softmax that needs it before
+// the choices are known (by value, or not renormalised); sum: the softmax's
+// where it is not renormalised.
+template <int P, bool WIDE>
+__device__ __forceinline__ int choose(const RouteArgs& a, int t, int lane, double* vals, float& zmax,
+                                      double& sum) {
+  Token<P> tk;
+  tk.row = static_cast<size_t>(t) * a.E;
+  if (a.bf16) {
+    const uint16_t* z = static_cast<const uint16_t*>(a.logits) + tk.row;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      tk.z[i] = __builtin_bit_cast(
+          float, static_cast<uint32_t>(z[min(expert_of<P, WIDE>(lane, i), a.E - 1)]) << 16);
+  } else {
+    const float* z = static_cast<const float*>(a.logits) + tk.row;
+#pragma unroll
+    for (int i = 0; i < P; ++i) tk.z[i] = z[min(expert_of<P, WIDE>(lane, i), a.E - 1)];
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    tk.live[i] = live_logit(tk.z[i]) && expert_of<P, WIDE>(lane, i) < a.E;
+  int id;
+  zmax = 0.f;
+  if (!a.sigmoid && (WIDE || !a.renormalize)) zmax = largest(tk);
+  if constexpr (WIDE) {
+    id = choose_by_value<P>(a, tk, zmax, lane, vals);
+  } else {
+    uint32_t key[P], rank;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      key[i] = tk.live[i] ? (order_key(tk.z[i]) & ~static_cast<uint32_t>(P - 1)) | (P - 1 - i) : 0;
+    // bf16 leaves the low bits free; fp32 keys may differ only there
+    auto apart = [&](uint32_t hi, uint32_t lo) { return a.bf16 || (hi ^ lo) >= P; };
+    const int n = take_packed<P, false>(key, a.top_k, lane, rank, id, apart);
+    const uint32_t before = __shfl_up(rank, 1);
+    if (n > 64) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) key[i] = tk.live[i] ? order_key(tk.z[i]) : 0;
+      id = take<P, false>(key, a.top_k, lane);
+    } else if (__any(lane > 0 && lane < n && !apart(before, rank))) {
+      float z = 0.f;
+      if (id >= 0) {
+        z = load_logit(a, tk.row + id);
+        live_logit(z);
+      }
+      id = in_order(id, z, n, lane);
+    }
+  }
+  sum = 1.0;
+  if (!a.sigmoid && !a.renormalize) {
     double part = 0.0;
 #pragma unroll
     for (int i = 0; i < P; ++i)
-      if (tk.live[i]) part += exp(static_cast<double>(tk.z[i]) - tk.zmax);
-    total = wave_sum_of(part);
+      if (tk.live[i]) part += exp(static_cast<double>(tk.z[i]) - zmax);
+    sum = wave_sum_of(part);
   }
-  weight = total > 0.0 ? static_cast<float>(s * static_cast<double>(a.scale) / total) : 0.f;
+  return id;
 }
 
 struct RouteLds {
   alignas(16) int ids[kRtMaxSlots];  // this chunk's, in whole groups of four
+  double score[kRtMaxSlots];         // the chosen experts'
+  double sum[kRtChunk];              // choose()'s, per token
+  float zmax[kRtChunk];
   int count[kRtMaxExperts];          // this chunk's slots per expert
   int total[kRtMaxExperts];          // all chunks'
   int before[kRtMaxExperts];         // the chunks' before this one; then the place of the first slot
@@ -441,18 +609,54 @@ __global__ __launch_bounds__(64 * W) void route_kernel(const RouteArgs a) {
   for (int e = tid; e < count_stride(a.E); e += 64 * W) l.count[e] = 0;
   __syncthreads();
   for (int i = wave; i < tokens; i += W) {
-    int id;
-    float w;
-    choose<P, WIDE>(a, t0 + i, lane, rt_vals + static_cast<size_t>(wave) * a.E, id, w);
+    float zmax;
+    double sum;
+    const int id =
+        choose<P, WIDE>(a, t0 + i, lane, rt_vals + static_cast<size_t>(wave) * a.E, zmax, sum);
     if (lane < a.top_k) {
-      const size_t s = static_cast<size_t>(t0 + i) * a.top_k + lane;
-      a.ids[s] = id;
-      a.weights[s] = w;
-      if constexpr (ONE) l.ids[i * a.top_k + lane] = id;
+      l.ids[i * a.top_k + lane] = id;
       if (id >= 0) atomicAdd(&l.count[id], 1);  // integer sums: the order does not matter
+    }
+    if (lane == 0) {
+      l.zmax[i] = zmax;
+      l.sum[i] = sum;
     }
   }
   __syncthreads();
+  // the weights, a thread per slot
+  const int n = tokens * a.top_k;
+  auto logit = [&](int s, int id) {
+    float z = load_logit(a, static_cast<size_t>(t0 + s / a.top_k) * a.E + id);
+    live_logit(z);
+    return z;
+  };
+  for (int s = tid; s < n; s += 64 * W) {
+    const int id = l.ids[s];
+    double score = 0.0;
+    if (id >= 0) {
+      const double z = logit(s, id);
+      if (a.sigmoid) {
+        score = 1.0 / (1.0 + exp(-z));
+      } else {
+        const int i = s / a.top_k;  // by logit the first choice has the largest
+        const float zmax = WIDE || !a.renormalize ? l.zmax[i] : logit(s, l.ids[i * a.top_k]);
+        score = exp(z - zmax);
+      }
+    }
+    l.score[s] = score;
+  }
+  __syncthreads();
+  for (int s = tid; s < n; s += 64 * W) {
+    const int i = s / a.top_k;
+    double total = l.sum[i];
+    if (a.renormalize) {  // the softmax's own sum cancels
+      total = 0.0;
+      for (int j = 0; j < a.top_k; ++j) total += l.score[i * a.top_k + j];
+    }
+    const size_t at = static_cast<size_t>(t0) * a.top_k + s;
+    a.ids[at] = l.ids[s];
+    a.weights[at] = total > 0.0 ? static_cast<float>(l.score[s] * static_cast<double>(a.scale) / total) : 0.f;
+  }
   if constexpr (ONE) {
     if (tid < a.E) {
       l.total[tid] = l.count[tid];
@@ -507,32 +711,35 @@ __global__ __launch_bounds__(kRtThreads) void route_list_kernel(const RouteArgs 
       l.total[tid] = a.sums[static_cast<size_t>(a.chunks) * a.E + tid];
     }
   } else {
-    if (tid < count_stride(a.E)) l.before[tid] = l.total[tid] = 0;
+    if (tid < count_stride(a.E)) l.total[tid] = 0;
     __syncthreads();
     // four experts (one word of a chunk's counts) per thread, the chunks dealt
-    // out over the threads left
+    // out over the threads left; a total and its part before this chunk share a
+    // word, at most kRtSumChunks * kRtChunk each
+    static_assert(kRtSumChunks * kRtChunk < 1 << 15, "two counts in a word");
     const int words = count_stride(a.E) / 4;
     int width = 1;
     while (width < words) width <<= 1;
     const int wd = tid & (width - 1), step = kRtThreads / width;
     if (wd < words) {
-      int tot[4] = {0, 0, 0, 0}, bef[4] = {0, 0, 0, 0};
+      uint32_t sum[4] = {0, 0, 0, 0};
       const uint32_t* h = reinterpret_cast<const uint32_t*>(a.counts) + wd;
-#pragma unroll 8
+#pragma unroll 16
       for (int r = tid / width; r < a.chunks; r += step) {
         const uint32_t v = h[static_cast<size_t>(r) * words];
+        const uint32_t twice = r < c ? 0x10001u : 1u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int x = (v >> (8 * i)) & 255;
-          tot[i] += x;
-          bef[i] += r < c ? x : 0;
-        }
+        for (int i = 0; i < 4; ++i) sum[i] += (v >> (8 * i) & 255) * twice;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (tot[i]) atomicAdd(&l.total[4 * wd + i], tot[i]);
-        if (bef[i]) atomicAdd(&l.before[4 * wd + i], bef[i]);
-      }
+      for (int i = 0; i < 4; ++i)
+        if (sum[i]) atomicAdd(&l.total[4 * wd + i], static_cast<int>(sum[i]));
+    }
+    __syncthreads();
+    if (tid < a.E) {
+      const uint32_t both = l.total[tid];
+      l.total[tid] = both & 0xFFFF;
+      l.before[tid] = both >> 16;
     }
   }
   __syncthreads();
@@ -645,11 +852,17 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(const CombineArgs a
 
 }  // namespace
 
+// Enough for every number of tokens up to T: chunks are larger for more tokens,
+// so the ends of the ranges count too.
 size_t route_workspace_bytes(int T, int E) {
-  if (route_one(T, E)) return 0;
-  size_t n = counts_bytes(T, E);
-  if (route_chunks(T) > kRtSumChunks) n += (static_cast<size_t>(route_chunks(T)) + 1) * E * sizeof(int);
-  return n;
+  size_t most = 0;
+  for (int t : {T < kRtFewTokens ? T : kRtFewTokens, T < kRtMidTokens ? T : kRtMidTokens, T}) {
+    if (route_one(t, E)) continue;
+    size_t n = counts_bytes(t, E);
+    if (route_chunks(t) > kRtSumChunks) n += (static_cast<size_t>(route_chunks(t)) + 1) * E * sizeof(int);
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
 hipError_t launch_route(RouteArgs a, hipStream_t stream) {
