@@ -48,7 +48,8 @@ __device__ __forceinline__ int t8_slot(int piece, int row) {
 // pieces coalesced (8 lanes a row) and turns them into operands through a
 // wave-private LDS area; read in operand order, a load's 16 consecutive lanes
 // sit in 16 rows, 16 cache lines for 256 bytes.
-template <int MB, int NB, int WAVES, bool XS>
+// ONCE: a single row tile reads the weights.
+template <int MB, int NB, int WAVES, bool XS, bool ONCE>
 __global__ __launch_bounds__(64 * WAVES) void w8a8_small_kernel(const W8A8Args a, int MT) {
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
@@ -84,8 +85,12 @@ __global__ __launch_bounds__(64 * WAVES) void w8a8_small_kernel(const W8A8Args a
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)  // past the last step: re-read, not used
-        st.w[h][nb] = __builtin_nontemporal_load(wbase[nb] + static_cast<size_t>(min(2 * s + h, S - 1)) * 64);
+      for (int nb = 0; nb < NB; ++nb) {  // past the last step: re-read, not used
+        const auto at = wbase[nb] + static_cast<size_t>(min(2 * s + h, S - 1)) * 64;
+        // several row tiles read them: kept in L2 (5120 x 17408, M = 64, two row
+        // tiles: 31.4 -> 29.2 us; one row, read once: 17.0 against 18.3)
+        st.w[h][nb] = ONCE ? __builtin_nontemporal_load(at) : *at;
+      }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -165,14 +170,15 @@ template <int MB, int NB, int WAVES, bool XS>
 hipError_t launch_small(const W8A8Args& a, hipStream_t stream) {
   const int NCB = (a.N + 15) / 16;
   const size_t lds = static_cast<size_t>(WAVES) * MB * 1024 * (XS && NB < 2 ? 2 : NB);
-  const void* fn = reinterpret_cast<const void*>(&w8a8_small_kernel<MB, NB, WAVES, XS>);
+  int MT = (a.M + 16 * MB - 1) / (16 * MB);
+  const void* fn = MT == 1 ? reinterpret_cast<const void*>(&w8a8_small_kernel<MB, NB, WAVES, XS, true>)
+                           : reinterpret_cast<const void*>(&w8a8_small_kernel<MB, NB, WAVES, XS, false>);
   if (lds >= 64 * 1024) {
     const hipError_t e =
         hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
     if (e != hipSuccess) return e;
   }
   W8A8Args args = a;
-  int MT = (a.M + 16 * MB - 1) / (16 * MB);
   void* kargs[] = {&args, &MT};
   return hipLaunchKernel(fn, dim3((NCB + NB - 1) / NB * MT), dim3(64 * WAVES), kargs, lds, stream);
 }
@@ -418,19 +424,22 @@ hipError_t launch_tile(const W8A8Args& a, hipStream_t stream) {
 }
 
 // The forms, by modelled time. Few rows: a workgroup streams its 16 (rows +
-// columns) x K operand bytes at about 45 GB/s after 2.5 us (a fifth less from
-// three workgroups per compute unit on), one round of workgroups after the
-// other, so the smallest rounds x (rows + columns) is best; where the
-// workgroups are few (a narrow N), one column block and 16 waves. Tiles:
-// per k-tile of 128 the n tiles of a compute unit take 0.6 us or 0.3 n (64 x
-// 64), 0.9 or 0.75 n (128 x 192, two workgroups at once) and 1.3 n (256 x 192). Measured on N x K =
-// 7168 x 5120, 5120 x 6144, 34816 x 5120, 5120 x 17408 and their eighths at M
-// = 1 to 2048 with every form; the one chosen is within 1.1 of the fastest
-// measured, mostly the fastest (1.3 once: 5120 x 2176, M = 128). For instance (us): 7168 x 5120, M = 128: 4 x 2
-// 23.1, 64 x 64 26.9, 128 x 192 37.1; M = 256: 64 x 64 28.3, 128 x 192 37.2;
-// 34816 x 5120, M = 64: 4 x 2 60.6, 64 x 64 41.3, 128 x 192 44.8; M = 512: 128
-// x 192 104, 256 x 192 106; M = 1024: 183, 161.
-enum W8A8Form : int { kS1x1, kS1x2, kS2x1, kS2x2, kS2x3, kS4x2, kS2x4, kT64x64, kT128x192, kT256x192 };
+// columns) x K operand bytes after 3 us, at about 45 GB/s where it alone reads
+// its weights and 60 GB/s where other row tiles read them too (a fifth less from
+// three workgroups per compute unit on), with a fixed cost per step as of eight
+// columns; one round of workgroups follows the other, so the smallest rounds x
+// (rows + columns) is best. Tiles: per k-tile of 128 the n tiles of a compute
+// unit take 0.6 us or 0.3 n (64 x 64), 0.9 or 0.75 n (128 x 192, two workgroups
+// at once) and 1.3 n (256 x 192). Measured on N x K = 7168 x 5120, 5120 x 6144,
+// 34816 x 5120, 5120 x 17408, their eighths and 12000 x 4096 at M = 1 to 512
+// with every form (to 2048 the tiles): the one chosen takes 1.007 times the
+// fastest measured in the mean and at most 1.18 (5120 x 2176, M = 32). For
+// instance (us): 5120 x 17408, M = 64: 2 x 3 27.1, 2 x 4 31.3, 64 x 64 85; M =
+// 128: 4 x 3 34.6, 2 x 3 45.1; 34816 x 5120, M = 64: 4 x 3 49.2, 64 x 64 41.1,
+// 128 x 192 45.8; 7168 x 5120, M = 256: 64 x 64 28.3, 128 x 192 37.2; 34816 x
+// 5120, M = 512: 128 x 192 104, 256 x 192 106; M = 1024: 183, 161. Forms of 2 x
+// 1 and 4 x 2 gained nothing over these.
+enum W8A8Form : int { kS1x1, kS1x2, kS2x2, kS2x3, kS2x4, kS4x3, kS4x4, kT64x64, kT128x192, kT256x192 };
 constexpr int kSmallMaxRows = 512;  // few-rows forms are not looked at above
 
 W8A8Form w8a8_form(int M, int N, int K) {
@@ -454,12 +463,12 @@ W8A8Form w8a8_form(int M, int N, int K) {
     const struct {
       W8A8Form f;
       int mb, nb;
-    } small[] = {{kS4x2, 4, 2}, {kS2x4, 2, 4}, {kS2x3, 2, 3}, {kS2x2, 2, 2}, {kS2x1, 2, 1}, {kS1x2, 1, 2}, {kS1x1, 1, 1}};
+    } small[] = {{kS4x4, 4, 4}, {kS4x3, 4, 3}, {kS2x4, 2, 4}, {kS2x3, 2, 3}, {kS2x2, 2, 2}, {kS1x2, 1, 2}, {kS1x1, 1, 1}};
     for (const auto& s : small) {  // of equal ones the first: fewest reads of the weights
       if (s.mb > 1 && M <= 8 * s.mb) continue;  // half the row blocks hold as many rows
       const double r = rounds(16 * s.mb, 16 * s.nb);
       const double rows = M < 16 * s.mb ? M : 16 * s.mb;
-      consider(s.f, 2.5 + r * (r >= 3 ? 1.2 : 1.0) * (rows + 16 * s.nb) * K / 45000.0);
+      consider(s.f, 3.0 + r * (r >= 3 ? 1.2 : 1.0) * (rows + 16 * s.nb + 8) * K / (M > 16 * s.mb ? 60000.0 : 45000.0));
     }
   }
   return best;
@@ -473,11 +482,11 @@ hipError_t launch_w8a8(const W8A8Args& a, hipStream_t stream) {
     // read in operand order up to 8 rows: 7.9 against 8.0 us at M = 1, N =
     // 7168, K = 5120, 4.7 against 5.9 at N = 896; at 16 rows 9.4 against 9.1
     case kS1x2: return a.M <= 8 ? launch_small<1, 2, 8, false>(a, stream) : launch_small<1, 2, 8, true>(a, stream);
-    case kS2x1: return launch_small<2, 1, 16, true>(a, stream);
     case kS2x2: return launch_small<2, 2, 8, true>(a, stream);
     case kS2x3: return launch_small<2, 3, 8, true>(a, stream);
-    case kS4x2: return launch_small<4, 2, 8, true>(a, stream);
     case kS2x4: return launch_small<2, 4, 8, true>(a, stream);
+    case kS4x3: return launch_small<4, 3, 8, true>(a, stream);
+    case kS4x4: return launch_small<4, 4, 8, true>(a, stream);
     case kT64x64: return launch_tile<2, 2, 2, 2>(a, stream);
     case kT128x192: return launch_tile<2, 4, 4, 3>(a, stream);
     default: return launch_tile<4, 2, 4, 6>(a, stream);
