@@ -20,7 +20,7 @@
 //    first weights need only the offsets and start beside it).
 //  * otherwise experts_tile_kernel, the R x 256 MFMA tile engine of the dense
 //    product with its rows gathered: 32-row tiles, bound by HBM while the
-//    experts have few rows each (5.4 TB/s at 37 tokens of 8 experts out of
+//    experts have few rows each (5.6 TB/s at 37 tokens of 8 experts out of
 //    128), 128-row tiles, bound by LDS reads and MFMA, when they have many.
 //
 // With SwiGLU a workgroup owns the same columns of the gate half and of the
@@ -378,8 +378,8 @@ struct ExTile {
 };
 
 // One row tile with MB x 16 row blocks of the tile engine, D k-tiles ahead;
-// slot_of names the output row of each tile row.
-template <int GS, int MB, int D, bool ACT>
+// slot_of names the output row of each tile row. ONCE: the expert's only tile.
+template <int GS, int MB, int D, bool ACT, bool ONCE = false>
 __device__ __forceinline__ void expert_tile(const ExpertsArgs& a, unsigned char* lds, const int* slot_of,
                                             const Place& pl, int nt) {
   using C = LgCfg<GS, MB>;
@@ -390,7 +390,7 @@ __device__ __forceinline__ void expert_tile(const ExpertsArgs& a, unsigned char*
   const int blk1 = ACT ? blk0 + NCB / 2 : blk0 + 1;
   const size_t words = static_cast<size_t>(NCB) * 16 * a.K / 8;
   const long long x_rows = (static_cast<long long>(a.slots) + a.x_div - 1) / a.x_div;
-  using Engine = TileEngine<GS, MB, true>;
+  using Engine = TileEngine<GS, MB, true, ONCE>;
   Engine e;
   e.setup_gathered(lds, a.x, static_cast<uint32_t>(x_rows * a.K * 2),
                    a.qweight + pl.expert * words, a.scales + static_cast<size_t>(pl.expert) * NCB * G * 16,
@@ -471,6 +471,8 @@ __global__ __launch_bounds__(kLgThreads, 1) void experts_tile_kernel(const Exper
     expert_tile<GS, MB, MB == 8 ? 1 : 2, ACT>(a, ex_tile_lds, slot_of, pl, nt);
   else if (MB > 2 && pl.count > 32)
     expert_tile<GS, MB == 2 ? 2 : 4, 2, ACT>(a, ex_tile_lds, slot_of, pl, nt);
+  else if (MB == 2 && pl.tiles == 1)
+    expert_tile<GS, 2, 2, ACT, true>(a, ex_tile_lds, slot_of, pl, nt);
   else
     expert_tile<GS, 2, 2, ACT>(a, ex_tile_lds, slot_of, pl, nt);
 }
@@ -505,8 +507,8 @@ hipError_t launch_tile_t(const ExpertsArgs& a, hipStream_t stream) {
 //     more from 2 rows per expert on (tiles past 4 rows)
 //   32-row tiles: 3 + k-tiles max(0.7, 0.3 + 0.0025 workgroups)
 // For instance (us, few rows against 32-row tiles, 128 experts): 2048 x 5120 at
-// 1 token 10.9 / 31.0, at 16 68 / 86, at 64 127 / 118; 5120 x 1024 at 1 token
-// 10.7 / 9.7, at 64 123 / 63. While there is at most one workgroup per compute
+// 1 token 11.2 / 31.9, at 16 86 / 84, at 64 140 / 113; 5120 x 1024 at 1 token
+// 12.0 / 10.5, at 64 136 / 68. While there is at most one workgroup per compute
 // unit, few rows takes 64 columns and 8 waves (2048 x 5120 at 1 token: 10.1).
 // 128-row tiles from 100 rows per expert on with two workgroups per compute
 // unit or more (32-row against 128-row: 2048 x 5120, 128 experts, mean 64: 299

@@ -75,7 +75,10 @@ __device__ __forceinline__ void zero(Acc<MB>& a) {
 // expert): setup_gathered takes each thread's byte offsets of the rows it
 // stages, and the two column blocks of every wave, instead of setup's
 // contiguous ones. The rest (kloop, kloop_deep, compute) is the same.
-template <int GS, int MB, bool GATHER = false>
+// ONCE: no other workgroup reads the weights, so they pass the caches by
+// (non-temporal; experts' products, 8 rows each of 128 experts, N = 2048, K =
+// 5120: 126 -> 116 us).
+template <int GS, int MB, bool GATHER = false, bool ONCE = false>
 struct TileEngine {
   using C = LgCfg<GS, MB>;
   unsigned char* lds;
@@ -179,6 +182,7 @@ struct TileEngine {
   __device__ __forceinline__ void load_b(BRegs<GS>& r, int t, int nb0 = 0, int nb1 = kLgNB) const {
     const uint32_t qlane = static_cast<uint32_t>(lane) * C::WPL * 4u;
     const uint32_t slane = static_cast<uint32_t>(lane & 14) * 2u;
+    constexpr int kCache = ONCE ? 2 : 0;  // the instruction's nt bit
 #pragma unroll
     for (int gi = 0; gi < C::T; ++gi) {
       int grp = t * C::T + gi;
@@ -189,15 +193,15 @@ struct TileEngine {
         const uint32_t tile_idx = static_cast<uint32_t>(blk[nb]) * G + grp;
         const int qoff = static_cast<int>(tile_idx * (64u * C::WPL * 4u));
         if constexpr (C::WPL == 4) {
-          u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rq, qlane, qoff, 0);
+          u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rq, qlane, qoff, kCache);
 #pragma unroll
           for (int w = 0; w < 4; ++w) r.w[nb][gi * 4 + w] = v[w];
         } else if constexpr (C::WPL == 2) {
-          u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(rq, qlane, qoff, 0);
+          u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(rq, qlane, qoff, kCache);
           r.w[nb][gi * 2 + 0] = v[0];
           r.w[nb][gi * 2 + 1] = v[1];
         } else {
-          r.w[nb][gi] = __builtin_amdgcn_raw_buffer_load_b32(rq, qlane, qoff, 0);
+          r.w[nb][gi] = __builtin_amdgcn_raw_buffer_load_b32(rq, qlane, qoff, kCache);
         }
         r.s[nb][gi] =
             __builtin_amdgcn_raw_buffer_load_b32(rs, slane, static_cast<int>(tile_idx * 32u), 0);
