@@ -286,3 +286,25 @@ def test_many_equal_values(E, groups, scoring):
     for b in (None, np.full(E, 0.25)):
         check_route(z, b, 8, scoring=scoring)
         check_route(z, b, 8, scoring=scoring, groups=groups, groups_kept=3, group_top=2)
+
+
+@pytest.mark.parametrize("T", [5, 40, 3000])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_bias_out_of_range_keeps_lists_whole(T, bad):
+    """A bias outside the interface's range: any choice, but distinct experts and
+    lists that agree with them."""
+    rng = np.random.default_rng(T)
+    E, k = 96, 8
+    z = rng.standard_normal((T, E)).astype(np.float32)
+    b = np.where(rng.random(E) < 0.3, bad, 0.1)
+    for kw in (dict(scoring="sigmoid"), dict(groups=8, groups_kept=4, group_top=2), dict(groups=3, groups_kept=2)):
+        ids, _, off, rows = run_route(z, b, k, **kw)
+        assert ids.min() >= -1 and ids.max() < E
+        for row in ids:
+            chosen = row[row >= 0]
+            assert len(set(chosen.tolist())) == len(chosen)
+        flat = ids.reshape(-1)
+        assert off[0] == 0 and off[E] == (flat >= 0).sum()
+        for e in range(E):
+            assert np.array_equal(rows[off[e]:off[e + 1]], np.flatnonzero(flat == e))
+        assert np.all(rows[off[E]:] == -1)

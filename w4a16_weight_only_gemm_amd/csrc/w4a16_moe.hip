@@ -349,7 +349,8 @@ __device__ __forceinline__ void choice_keys(const RouteArgs& a, const Token<P>& 
       v[i] += static_cast<S>(a.bias[min(expert_of<P, true>(lane, i), a.E - 1)]);
   }
 #pragma unroll
-  for (int i = 0; i < P; ++i) key[i] = tk.live[i] ? order_key(v[i]) : 0;
+  for (int i = 0; i < P; ++i)  // a NaN (from the bias) has no place in an order
+    key[i] = tk.live[i] && v[i] == v[i] ? order_key(v[i]) : 0;
 }
 
 // Whether fp32 values hi >= lo are further apart than their errors.
@@ -376,6 +377,8 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs& a, Key (&key)[P], f
 #pragma unroll
     for (int i = 0; i < P; ++i) put(key[i]);
   } else {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // behind the reads of an earlier use
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int i = 0; i < P; ++i)
       if (lane * P + i < a.E) vals[lane * P + i] = key[i];
