@@ -26,6 +26,20 @@ __device__ __forceinline__ gptr<T> to_global(T* p) {
   return (gptr<T>)(p);  // address-space cast (generic to global)
 }
 
+// Eight bf16 of a row of y, or the first `left` of them at the row's end. Rows
+// may start at any even address: the card's 16-byte global accesses need no
+// more alignment than an element's.
+__device__ __forceinline__ void store_piece(gptr<uint16_t> y, u32x4 v, int left) {
+  typedef uint32_t piece __attribute__((ext_vector_type(4), aligned(2)));
+  if (left >= 8) {
+    *reinterpret_cast<gptr<piece>>(y) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < left) y[i] = static_cast<uint16_t>(v[i / 2] >> (16 * (i % 2)));
+  }
+}
+
 // A value read through the constant address space: the memory must not be
 // written while the kernel runs (a plan's problem table), and a uniform
 // address then becomes a scalar load into SGPRs.

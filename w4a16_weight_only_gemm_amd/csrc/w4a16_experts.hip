@@ -302,7 +302,10 @@ __global__ __launch_bounds__(64 * WAVES) void experts_small_kernel(const Experts
       else
         stream(std::integral_constant<int, 4>{}, std::integral_constant<int, P16>{});
     } else {
-      stream(std::integral_constant<int, 4>{}, std::integral_constant<int, P16>{});
+      // groups of 32 and 64: more of them ahead, as they are smaller (784 x
+      // 4352, group 32, 1 token of 8 experts: 16.7 -> 11.6 us)
+      constexpr int kAhead = GS == 32 ? 8 : GS == 64 ? 4 : P16;
+      stream(std::integral_constant<int, 4>{}, std::integral_constant<int, kAhead>{});
     }
   }
   if (static_cast<int>(threadIdx.x) < TM) {
@@ -428,22 +431,12 @@ __device__ __forceinline__ void expert_tile(const ExpertsArgs& a, unsigned char*
   __syncthreads();
   const int out_cols = ACT ? a.N / 2 : a.N, col0 = nt * Cols;
   gptr<uint16_t> yg = to_global(a.y);
-  if (out_cols % 8 == 0) {  // rows keep 16-byte alignment, pieces are in or out whole
-    for (int i = threadIdx.x; i < MB * 16 * (Cols / 8); i += kLgThreads) {
-      const int r = i / (Cols / 8), col = i % (Cols / 8) * 8;
-      const int s = slot_of[r];
-      if (s >= 0 && col0 + col < out_cols)
-        *reinterpret_cast<gptr<u32x4>>(yg + static_cast<size_t>(s) * out_cols + col0 + col) =
-            *reinterpret_cast<const u32x4*>(lds + r * Stride + col * 2);
-    }
-  } else {
-    for (int i = threadIdx.x; i < MB * 16 * Cols; i += kLgThreads) {
-      const int r = i / Cols, col = i % Cols;
-      const int s = slot_of[r];
-      if (s >= 0 && col0 + col < out_cols)
-        yg[static_cast<size_t>(s) * out_cols + col0 + col] =
-            *reinterpret_cast<const uint16_t*>(lds + r * Stride + col * 2);
-    }
+  for (int i = threadIdx.x; i < MB * 16 * (Cols / 8); i += kLgThreads) {
+    const int r = i / (Cols / 8), col = i % (Cols / 8) * 8;
+    const int s = slot_of[r], left = out_cols - (col0 + col);
+    if (s < 0 || left <= 0) continue;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(lds + r * Stride + col * 2);
+    store_piece(yg + static_cast<size_t>(s) * out_cols + col0 + col, v, left);
   }
 }
 

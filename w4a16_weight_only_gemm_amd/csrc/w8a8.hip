@@ -171,8 +171,9 @@ hipError_t launch_small(const W8A8Args& a, hipStream_t stream) {
   const int NCB = (a.N + 15) / 16;
   const size_t lds = static_cast<size_t>(WAVES) * MB * 1024 * (XS && NB < 2 ? 2 : NB);
   int MT = (a.M + 16 * MB - 1) / (16 * MB);
+  // read in operand order there is one row tile
   const void* fn = MT == 1 ? reinterpret_cast<const void*>(&w8a8_small_kernel<MB, NB, WAVES, XS, true>)
-                           : reinterpret_cast<const void*>(&w8a8_small_kernel<MB, NB, WAVES, XS, false>);
+                           : reinterpret_cast<const void*>(&w8a8_small_kernel<MB, NB, WAVES, XS, !XS>);
   if (lds >= 64 * 1024) {
     const hipError_t e =
         hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
@@ -383,23 +384,14 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void w8a8_tile_kernel(co
       }
       *reinterpret_cast<u32x2*>(part + c16 * Stride + nb * 32 + lg * 8) = o;
     }
-    if (a.N % 8 == 0) {  // rows keep 16-byte alignment, pieces are in or out whole
-      constexpr int Pieces = NB * 2;  // per row
+    constexpr int Pieces = NB * 2;  // per row
 #pragma unroll
-      for (int i = 0; i < (16 * Pieces + 63) / 64; ++i) {
-        const int e = i * 64 + lane, row = e / Pieces, col = e % Pieces * 8;
-        if (e >= 16 * Pieces) continue;
-        const u32x4 v = *reinterpret_cast<const u32x4*>(part + row * Stride + col * 2);
-        if (row0 + row < a.M && n0 + col < a.N)
-          *reinterpret_cast<gptr<u32x4>>(to_global(a.y) + static_cast<size_t>(row0 + row) * a.N + n0 + col) = v;
-      }
-    } else {
-      for (int e = lane; e < 16 * NB * 16; e += 64) {
-        const int row = e / (NB * 16), col = e % (NB * 16);
-        const uint16_t v = *reinterpret_cast<const uint16_t*>(part + row * Stride + col * 2);
-        if (row0 + row < a.M && n0 + col < a.N)
-          to_global(a.y)[static_cast<size_t>(row0 + row) * a.N + n0 + col] = v;
-      }
+    for (int i = 0; i < (16 * Pieces + 63) / 64; ++i) {
+      const int e = i * 64 + lane, row = e / Pieces, col = e % Pieces * 8;
+      if (e >= 16 * Pieces) continue;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(part + row * Stride + col * 2);
+      if (row0 + row < a.M && n0 + col < a.N)
+        store_piece(to_global(a.y) + static_cast<size_t>(row0 + row) * a.N + n0 + col, v, a.N - (n0 + col));
     }
   }
 }
