@@ -308,3 +308,25 @@ def test_bias_out_of_range_keeps_lists_whole(T, bad):
         for e in range(E):
             assert np.array_equal(rows[off[e]:off[e + 1]], np.flatnonzero(flat == e))
         assert np.all(rows[off[E]:] == -1)
+
+
+@pytest.mark.parametrize("T,k,N", [(1, 2, 8), (3, 1, 9), (40, 3, 15), (700, 3, 1209), (90, 8, 4588)])
+def test_combine_rows_at_any_address(T, k, N):
+    """Rows that start between 16-byte borders; nothing is written behind the last."""
+    import torch
+
+    import w4a16_weight_only_gemm_amd as w4
+    log("combine", T, k, N)
+    g = torch.Generator().manual_seed(N)
+    y = torch.randn(T * k, N, generator=g).to(torch.bfloat16)
+    b = torch.randn(T, N, generator=g).to(torch.bfloat16)
+    w = torch.rand(T, k, generator=g)
+    ids = torch.randint(-1, 5, (T, k), generator=g, dtype=torch.int32)
+    ref, tol = moe_ref.combine(y.double().numpy(), ids.numpy(), w.double().numpy(), b.double().numpy())
+    buf = torch.full((T * N + 64,), -5.0, dtype=torch.bfloat16, device="cuda")
+    buf[:T * N] = b.cuda().reshape(-1)
+    out = buf[:T * N].view(T, N)  # in place
+    w4.w4a16_moe_combine(y.cuda(), ids.cuda(), w.cuda(), out, out, T, k, N)
+    torch.cuda.synchronize()
+    moe_ref.check(out.view(torch.int16).cpu().numpy().view(np.uint16), ref, tol)
+    assert bool((buf[T * N:] == -5.0).all())
