@@ -72,12 +72,20 @@ def test_depths(M, K):
     (1, 200, 1040), (5, 5000, 656), (12, 5000, 656),          # one row block by one and two
     (120, 800, 1040), (30, 7000, 656), (60, 3500, 1040),      # also several row tiles; two by two
     (60, 7000, 656), (60, 5000, 1040), (90, 5000, 1040),      # two by four and three
-    (120, 5000, 656), (101, 5010, 656), (64, 11000, 400),     # four by three
-    (190, 5000, 784), (437, 1811, 784),                       # four by four
-    (520, 1000, 272), (1100, 2950, 144), (1090, 2957, 208),   # tiles of 64 x 64 and 128 x 192
+    (120, 5000, 656), (101, 5010, 656), (64, 11000, 400),     # tiles of 64 x 64
+    (190, 5000, 784), (437, 1811, 784), (64, 9000, 2064),
+    (520, 1000, 272), (1100, 2950, 144), (1090, 2957, 208),   # 64 x 64 and 128 x 128
     (4000, 2950, 144), (3970, 2941, 272), (4090, 2944, 64)])  # 256 x 192
 def test_every_form(M, N, K):
     check(M, N, K, seed=M + N)
+
+
+@pytest.mark.parametrize("K", [48, 144, 272, 400, 544, 656, 784, 1040])
+@pytest.mark.parametrize("M,N", [(553, 217), (66, 8555), (135, 11790), (261, 12069), (654, 11010)])
+def test_k_tiles(M, N, K):
+    """The tiles (64 x 64, 64 x 128, 128 x 128, 128 x 192, 256 x 192) over fewer
+    k-tiles of 128 than they hold buffers, as many, and more; the last one partial."""
+    check(M, N, K, seed=K)
 
 
 @pytest.mark.parametrize("M", [1, 130])

@@ -12,8 +12,8 @@
 //    HBM once. Bound by HBM.
 //  * w8a8_tile_kernel (many rows): a workgroup owns a row x column tile; its
 //    waves form WM x WN and each an MB x NB grid of 16 x 16 blocks. Both
-//    operands are copied to LDS (double-buffered). Bound by the rate of those
-//    copies and by MFMA.
+//    operands are copied to LDS, one to three k-tiles ahead. Bound by the rate
+//    of those copies and by MFMA.
 //
 // The last k step may be partial: its weight codes past K are zero, so the
 // activation codes there may be anything; their addresses are clamped into the
@@ -188,7 +188,7 @@ hipError_t launch_small(const W8A8Args& a, hipStream_t stream) {
 
 constexpr int kT8KT = 128;  // k per k-tile: two matrix-instruction steps
 
-template <int WM, int WN, int MB, int NB>
+template <int WM, int WN, int MB, int NB, int BUFS>
 struct T8Cfg {
   static constexpr int Waves = WM * WN;
   static constexpr int Threads = 64 * Waves;
@@ -198,8 +198,8 @@ struct T8Cfg {
   static constexpr int Loads = (Pieces + Waves - 1) / Waves;   // per wave
   static constexpr int ABytes = Rows * kT8KT;
   static constexpr int BufBytes = ABytes + Blocks * 2048;
-  static constexpr size_t Lds = 2 * static_cast<size_t>(BufBytes);
-  static_assert(Lds <= 160 * 1024, "both buffers fit");
+  static constexpr size_t Lds = BUFS * static_cast<size_t>(BufBytes);
+  static_assert(Lds <= 160 * 1024, "the buffers fit");
 };
 
 typedef int rsrc4 __attribute__((ext_vector_type(4)));
@@ -230,16 +230,27 @@ __device__ __forceinline__ void copy_to_lds(uint32_t lds, uint32_t voff, rsrc4 r
       : "memory");
 }
 
+// Waits until at most N of the wave's loads are on their way.
+template <int N>
+__device__ __forceinline__ void wait_vmem_but() {
+  static_assert(N < 64, "the counter has six bits");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+}
+
 // A workgroup's tile is (16 MB WM) rows x (16 NB WN) columns; k advances in
-// k-tiles of 128. Both operands of a k-tile are copied to one of two LDS
+// k-tiles of 128. Both operands of a k-tile are copied to one of BUFS LDS
 // buffers: activation rows of 128 bytes with their 16-byte pieces permuted by
 // t8_slot on the way (the lanes read permuted addresses of the same cache
 // lines), weight tiles as they lie. Per k-tile a wave reads 2 (MB + NB)
 // operands for 2 MB NB matrix instructions, those of half a k-tile while the
 // half before it multiplies. The one barrier per k-tile sits between the
 // halves: behind it, every wave has read the current buffer, which is refilled
-// with the k-tile after next, and the next buffer, whose copies were issued
-// one k-tile earlier, is complete.
+// with the k-tile BUFS further on, and the next buffer, whose copies were
+// issued BUFS - 1 k-tiles earlier, is complete. A compute unit that holds one
+// workgroup waits for its copies with two buffers; four instead of two: 7168 x
+// 5120, M = 128, 64 x 64 tiles 26.1 -> 14.5 us, M = 512, 128 x 128 33.4 -> 26.2;
+// three for 128 x 192: 5120 x 17408, M = 1024 114 -> 92 us, but 176 -> 198 at
+// 34816 x 5120, M = 1024, where two workgroups of two buffers share one.
 //
 // Copies and operand reads are dealt out among the matrix instructions: issued
 // in one run, the copies queue up in front of the address unit (16 cycles for
@@ -247,12 +258,11 @@ __device__ __forceinline__ void copy_to_lds(uint32_t lds, uint32_t voff, rsrc4 r
 // 34816, K = 5120, 256 x 192 tiles: 188 -> 173 us (2,110 TOP/s; a library
 // product of 8192^3 reaches 2,135 on the same card). There the matrix
 // instructions alone take 117 us and with the operand reads 135: the copies'
-// rate, about 20 bytes a cycle and compute unit, bounds the rest. Five
-// buffers in place of two, and copies through registers, were not faster (198
-// and 189 us).
-template <int WM, int WN, int MB, int NB>
+// rate, about 20 bytes a cycle and compute unit, bounds the rest. Copies
+// through registers were not faster (189 us).
+template <int WM, int WN, int MB, int NB, int BUFS>
 __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void w8a8_tile_kernel(const W8A8Args a, int MT, int NT) {
-  using C = T8Cfg<WM, WN, MB, NB>;
+  using C = T8Cfg<WM, WN, MB, NB, BUFS>;
   extern __shared__ __attribute__((aligned(16))) unsigned char t8_lds[];
   const int tile = xcd_grouped(blockIdx.x, MT * NT);
   const int mt = tile % MT, nt = tile / MT;
@@ -285,15 +295,15 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void w8a8_tile_kernel(co
   const uint32_t wbytes = static_cast<uint32_t>(NCB) * static_cast<uint32_t>(S) * 1024u;
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
       (__attribute__((address_space(3))) unsigned char*)t8_lds));
-  // part g of G of k-tile t's copies
-  auto copy = [&](int t, int g, int G) {
+  // part g of G of k-tile t's copies, into buffer b
+  auto copy = [&](int t, int b, int g, int G) {
     const rsrc4 rx = raw_rsrc(xbase + static_cast<size_t>(t) * kT8KT, xbytes - static_cast<uint32_t>(t) * kT8KT);
     const rsrc4 rw = raw_rsrc(a.qweight + static_cast<size_t>(t) * 2048, wbytes - static_cast<uint32_t>(t) * 2048u);
 #pragma unroll
     for (int i = 0; i < C::Loads; ++i) {
       if (i * G / C::Loads != g) continue;
       const int c = min(wave + C::Waves * i, C::Pieces - 1);
-      copy_to_lds(lds0 + (t & 1) * C::BufBytes + c * 1024, off[i], c < C::Rows / 8 ? rx : rw);
+      copy_to_lds(lds0 + b * C::BufBytes + c * 1024, off[i], c < C::Rows / 8 ? rx : rw);
     }
   };
 
@@ -304,7 +314,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void w8a8_tile_kernel(co
   const unsigned char* const wfrag = t8_lds + C::ABytes + wn * NB * 2048 + lane * 16;
   // part g of G of the operands of half s of k-tile t
   auto read = [&](Half& h, int t, int s, int g, int G) {
-    const int buf = (t & 1) * C::BufBytes;
+    const int buf = t % BUFS * C::BufBytes;
 #pragma unroll
     for (int i = 0; i < MB + NB; ++i) {
       if (i * G / (MB + NB) != g) continue;
@@ -325,10 +335,10 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void w8a8_tile_kernel(co
   };
 
   Half h0, h1;
-  copy(0, 0, 1);
-  wait_vmem_all();
+#pragma unroll
+  for (int i = 0; i < BUFS; ++i) copy(min(i, KT - 1), i, 0, 1);  // past the last: not read
+  wait_vmem_but<(BUFS - 1) * C::Loads>();
   lds_barrier();
-  if (KT > 1) copy(1, 0, 1);
   read(h0, 0, 0, 0, 1);
   auto tile_of = [&](int t, auto refill) {
 #pragma unroll
@@ -338,11 +348,12 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void w8a8_tile_kernel(co
       multiply(h0, g);
       __builtin_amdgcn_sched_barrier(0);
     }
-    wait_vmem_all();  // k-tile t + 1 has landed
-    lds_barrier();    // everywhere, and k-tile t has been read
+    // k-tile t + 1 has landed, everywhere, and k-tile t has been read
+    wait_vmem_but<refill ? (BUFS - 2) * C::Loads : 0>();
+    lds_barrier();
 #pragma unroll
     for (int g = 0; g < MB; ++g) {
-      if constexpr (refill) copy(t + 2, g, MB);
+      if constexpr (refill) copy(t + BUFS, t % BUFS, g, MB);
       read(h0, t + 1, 0, g, MB);         // past the last: not used
       __builtin_amdgcn_sched_barrier(0);
       if (2 * t + 1 < S) multiply(h1, g);  // else: the last k-tile has one step
@@ -350,7 +361,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void w8a8_tile_kernel(co
     }
   };
   int t = 0;
-  for (; t + 2 < KT; ++t) tile_of(t, std::true_type{});
+  for (; t + BUFS < KT; ++t) tile_of(t, std::true_type{});
   for (; t < KT; ++t) tile_of(t, std::false_type{});
 
   // The accumulator of lane l holds columns 4 (l / 16) .. + 3 of row l % 16 of
@@ -396,16 +407,16 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void w8a8_tile_kernel(co
   }
 }
 
-template <int WM, int WN, int MB, int NB>
+template <int WM, int WN, int MB, int NB, int BUFS>
 hipError_t launch_tile(const W8A8Args& a, hipStream_t stream) {
-  using C = T8Cfg<WM, WN, MB, NB>;
+  using C = T8Cfg<WM, WN, MB, NB, BUFS>;
   const int NCB = (a.N + 15) / 16;
   int MT = static_cast<int>((static_cast<long long>(a.M) + C::Rows - 1) / C::Rows);
   int NT = (NCB + C::Blocks - 1) / C::Blocks;
   const long long blocks = static_cast<long long>(MT) * NT;
   if (blocks * C::Threads > 0xFFFFFFFFLL) return hipErrorNotSupported;
-  const void* fn = reinterpret_cast<const void*>(&w8a8_tile_kernel<WM, WN, MB, NB>);
-  if (C::Lds > 64 * 1024) {
+  const void* fn = reinterpret_cast<const void*>(&w8a8_tile_kernel<WM, WN, MB, NB, BUFS>);
+  if (C::Lds >= 64 * 1024) {
     const hipError_t e =
         hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::Lds));
     if (e != hipSuccess) return e;
@@ -420,18 +431,16 @@ hipError_t launch_tile(const W8A8Args& a, hipStream_t stream) {
 // its weights and 60 GB/s where other row tiles read them too (a fifth less from
 // three workgroups per compute unit on), with a fixed cost per step as of eight
 // columns; one round of workgroups follows the other, so the smallest rounds x
-// (rows + columns) is best. Tiles: per k-tile of 128 the n tiles of a compute
-// unit take 0.6 us or 0.3 n (64 x 64), 0.9 or 0.75 n (128 x 192, two workgroups
-// at once) and 1.3 n (256 x 192). Measured on N x K = 7168 x 5120, 5120 x 6144,
-// 34816 x 5120, 5120 x 17408, their eighths and 12000 x 4096 at M = 1 to 512
-// with every form (to 2048 the tiles): the one chosen takes 1.007 times the
-// fastest measured in the mean and at most 1.18 (5120 x 2176, M = 32). For
-// instance (us): 5120 x 17408, M = 64: 2 x 3 27.1, 2 x 4 31.3, 64 x 64 85; M =
-// 128: 4 x 3 34.6, 2 x 3 45.1; 34816 x 5120, M = 64: 4 x 3 49.2, 64 x 64 41.1,
-// 128 x 192 45.8; 7168 x 5120, M = 256: 64 x 64 28.3, 128 x 192 37.2; 34816 x
-// 5120, M = 512: 128 x 192 104, 256 x 192 106; M = 1024: 183, 161. Forms of 2 x
-// 1 and 4 x 2 gained nothing over these.
-enum W8A8Form : int { kS1x1, kS1x2, kS2x2, kS2x3, kS2x4, kS4x3, kS4x4, kT64x64, kT128x192, kT256x192 };
+// (rows + columns) is best. Tiles: 3 us and a time per k-tile and round of
+// workgroups. Measured on N x K = 7168 x 5120, 5120 x 6144, 34816 x 5120, 5120 x
+// 17408, their eighths, 12000 x 4096, 2756 x 10368, 21968 x 1408, 710 x 17408 and
+// 1500 x 704 at M = 17 to 2048 with every form: the one chosen takes 1.011 times
+// the fastest measured in the mean and at most 1.16. For instance (us): 5120 x
+// 17408, M = 64: 2 x 3 blocks 27.1, 2 x 4 31.3; M = 256: 64 x 128 55, 64 x 64 63,
+// 128 x 128 72; 34816 x 5120, M = 64: 128 x 192 37, 64 x 128 50, 2 x 4
+// blocks 61; M = 512: 128 x 192 98, 256 x 192 103; M = 1024: 195, 155. Forms of 2 x 1, 4 x 2, 4 x 3 and 4 x
+// 4 blocks and of 64 x 192 gained 1 % or less over these.
+enum W8A8Form : int { kS1x1, kS1x2, kS2x2, kS2x3, kS2x4, kT64x64, kT64x128, kT128x128, kT128x192, kT256x192 };
 constexpr int kSmallMaxRows = 512;  // few-rows forms are not looked at above
 
 W8A8Form w8a8_form(int M, int N, int K) {
@@ -440,29 +449,33 @@ W8A8Form w8a8_form(int M, int N, int K) {
     return static_cast<double>((tiles + kModelCUs - 1) / kModelCUs);
   };
   const double kt = (K + kT8KT - 1) / kT8KT;
-  const double r64 = rounds(64, 64), r128 = rounds(128, 192), r256 = rounds(256, 192);
-  W8A8Form best = kT64x64;
-  double t = 1.0 + kt * (0.3 * r64 > 0.6 ? 0.3 * r64 : 0.6);
+  const struct {
+    W8A8Form f;
+    int rows, cols;
+    double us;  // per k-tile and round
+  } tiles[] = {{kT256x192, 256, 192, 1.15}, {kT128x192, 128, 192, 0.64}, {kT128x128, 128, 128, 0.49},
+               {kT64x128, 64, 128, 0.36}, {kT64x64, 64, 64, 0.24}};
+  const struct {
+    W8A8Form f;
+    int mb, nb;
+  } small[] = {{kS2x4, 2, 4}, {kS2x3, 2, 3}, {kS2x2, 2, 2}, {kS1x2, 1, 2}, {kS1x1, 1, 1}};
+  W8A8Form best = kT256x192;
+  double t = 1e30;  // of equal ones the first: fewest reads of the operands
   auto consider = [&](W8A8Form f, double us) {
     if (us < t) {
       best = f;
       t = us;
     }
   };
-  consider(kT128x192, 1.0 + kt * (0.75 * r128 > 0.9 ? 0.75 * r128 : 0.9));
-  consider(kT256x192, 1.0 + kt * 1.3 * r256);
-  if (M <= kSmallMaxRows) {
-    const struct {
-      W8A8Form f;
-      int mb, nb;
-    } small[] = {{kS4x4, 4, 4}, {kS4x3, 4, 3}, {kS2x4, 2, 4}, {kS2x3, 2, 3}, {kS2x2, 2, 2}, {kS1x2, 1, 2}, {kS1x1, 1, 1}};
-    for (const auto& s : small) {  // of equal ones the first: fewest reads of the weights
+  for (const auto& s : tiles)
+    if (M > 16) consider(s.f, 3.0 + kt * s.us * rounds(s.rows, s.cols));
+  if (M <= kSmallMaxRows)
+    for (const auto& s : small) {
       if (s.mb > 1 && M <= 8 * s.mb) continue;  // half the row blocks hold as many rows
       const double r = rounds(16 * s.mb, 16 * s.nb);
       const double rows = M < 16 * s.mb ? M : 16 * s.mb;
       consider(s.f, 3.0 + r * (r >= 3 ? 1.2 : 1.0) * (rows + 16 * s.nb + 8) * K / (M > 16 * s.mb ? 60000.0 : 45000.0));
     }
-  }
   return best;
 }
 
@@ -477,11 +490,11 @@ hipError_t launch_w8a8(const W8A8Args& a, hipStream_t stream) {
     case kS2x2: return launch_small<2, 2, 8, true>(a, stream);
     case kS2x3: return launch_small<2, 3, 8, true>(a, stream);
     case kS2x4: return launch_small<2, 4, 8, true>(a, stream);
-    case kS4x3: return launch_small<4, 3, 8, true>(a, stream);
-    case kS4x4: return launch_small<4, 4, 8, true>(a, stream);
-    case kT64x64: return launch_tile<2, 2, 2, 2>(a, stream);
-    case kT128x192: return launch_tile<2, 4, 4, 3>(a, stream);
-    default: return launch_tile<4, 2, 4, 6>(a, stream);
+    case kT64x64: return launch_tile<2, 2, 2, 2, 4>(a, stream);
+    case kT64x128: return launch_tile<2, 2, 2, 4, 4>(a, stream);
+    case kT128x128: return launch_tile<2, 4, 4, 2, 4>(a, stream);
+    case kT128x192: return launch_tile<2, 4, 4, 3, 3>(a, stream);
+    default: return launch_tile<4, 2, 4, 6, 2>(a, stream);
   }
 }
 
