@@ -81,10 +81,12 @@ def test_every_form(M, N, K):
 
 
 @pytest.mark.parametrize("K", [48, 144, 272, 400, 544, 656, 784, 1040])
-@pytest.mark.parametrize("M,N", [(553, 217), (66, 8555), (135, 11790), (261, 12069), (654, 11010)])
+@pytest.mark.parametrize("M,N", [(553, 217), (66, 8555), (135, 11790), (389, 12643), (261, 12069),
+                                 (775, 12447), (654, 11010)])
 def test_k_tiles(M, N, K):
-    """The tiles (64 x 64, 64 x 128, 128 x 128, 128 x 192, 256 x 192) over fewer
-    k-tiles of 128 than they hold buffers, as many, and more; the last one partial."""
+    """The tiles (64 x 64, 64 x 128, 128 x 128 and 128 x 192 with many and with two
+    buffers, 256 x 192) over fewer k-tiles of 128 than they hold buffers, as many,
+    and more; the last one partial."""
     check(M, N, K, seed=K)
 
 

@@ -314,7 +314,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void w8a8_tile_kernel(co
   const unsigned char* const wfrag = t8_lds + C::ABytes + wn * NB * 2048 + lane * 16;
   // part g of G of the operands of half s of k-tile t
   auto read = [&](Half& h, int t, int s, int g, int G) {
-    const int buf = t % BUFS * C::BufBytes;
+    const int buf = static_cast<unsigned>(t) % BUFS * C::BufBytes;
 #pragma unroll
     for (int i = 0; i < MB + NB; ++i) {
       if (i * G / (MB + NB) != g) continue;
@@ -353,7 +353,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void w8a8_tile_kernel(co
     lds_barrier();
 #pragma unroll
     for (int g = 0; g < MB; ++g) {
-      if constexpr (refill) copy(t + BUFS, t % BUFS, g, MB);
+      if constexpr (refill) copy(t + BUFS, static_cast<unsigned>(t) % BUFS, g, MB);
       read(h0, t + 1, 0, g, MB);         // past the last: not used
       __builtin_amdgcn_sched_barrier(0);
       if (2 * t + 1 < S) multiply(h1, g);  // else: the last k-tile has one step
@@ -431,16 +431,19 @@ hipError_t launch_tile(const W8A8Args& a, hipStream_t stream) {
 // its weights and 60 GB/s where other row tiles read them too (a fifth less from
 // three workgroups per compute unit on), with a fixed cost per step as of eight
 // columns; one round of workgroups follows the other, so the smallest rounds x
-// (rows + columns) is best. Tiles: 3 us and a time per k-tile and round of
-// workgroups. Measured on N x K = 7168 x 5120, 5120 x 6144, 34816 x 5120, 5120 x
-// 17408, their eighths, 12000 x 4096, 2756 x 10368, 21968 x 1408, 710 x 17408 and
-// 1500 x 704 at M = 17 to 2048 with every form: the one chosen takes 1.011 times
-// the fastest measured in the mean and at most 1.16. For instance (us): 5120 x
-// 17408, M = 64: 2 x 3 blocks 27.1, 2 x 4 31.3; M = 256: 64 x 128 55, 64 x 64 63,
-// 128 x 128 72; 34816 x 5120, M = 64: 128 x 192 37, 64 x 128 50, 2 x 4
-// blocks 61; M = 512: 128 x 192 98, 256 x 192 103; M = 1024: 195, 155. Forms of 2 x 1, 4 x 2, 4 x 3 and 4 x
-// 4 blocks and of 64 x 192 gained 1 % or less over these.
-enum W8A8Form : int { kS1x1, kS1x2, kS2x2, kS2x3, kS2x4, kT64x64, kT64x128, kT128x128, kT128x192, kT256x192 };
+// columns) is best. Tiles: 3 us and a time per k-tile and round of workgroups;
+// 128 x 128 and 128 x 192 hold more buffers while there is one round, and from
+// two on two buffers, so that two workgroups share a compute unit. Measured on N
+// x K = 7168 x 5120, 5120 x 6144, 34816 x 5120, 5120 x 17408, their eighths, 12000
+// x 4096, 2756 x 10368, 21968 x 1408, 710 x 17408 and 1500 x 704 at M = 17 to 4096
+// with every form: the one chosen takes 1.004 times the fastest measured in the
+// mean and at most 1.11. For instance (us): 5120 x 17408, M = 64: 2 x 3 blocks
+// 27.1, 2 x 4 31.3; M = 256: 64 x 128 55, 64 x 64 63, 128 x 128 72; 34816 x 5120, M
+// = 64: 128 x 192 37, 64 x 128 50, 2 x 4 blocks 61; M = 512: 128 x 192 98, 256 x
+// 192 103; M = 1024: 175, 155; 7168 x 5120, M = 2048: 128 x 192 with two buffers
+// 82, with three 92. Forms of 2 x 1, 4 x 2, 4 x 3 and 4 x 4 blocks and of 64 x 192
+// gained 1 % or less over these.
+enum W8A8Form : int { kS1x1, kS1x2, kS2x2, kS2x3, kS2x4, kT64x64, kT64x128, kT128x128, kT128x128Shared, kT128x192, kT128x192Shared, kT256x192 };
 constexpr int kSmallMaxRows = 512;  // few-rows forms are not looked at above
 
 W8A8Form w8a8_form(int M, int N, int K) {
@@ -452,9 +455,12 @@ W8A8Form w8a8_form(int M, int N, int K) {
   const struct {
     W8A8Form f;
     int rows, cols;
-    double us;  // per k-tile and round
-  } tiles[] = {{kT256x192, 256, 192, 1.15}, {kT128x192, 128, 192, 0.64}, {kT128x128, 128, 128, 0.49},
-               {kT64x128, 64, 128, 0.36}, {kT64x64, 64, 64, 0.24}};
+    double us;          // per k-tile and round
+    bool one, several;  // rounds it is for
+  } tiles[] = {{kT256x192, 256, 192, 1.1, true, true},         {kT128x192Shared, 128, 192, 0.66, false, true},
+               {kT128x192, 128, 192, 0.64, true, false},       {kT128x128Shared, 128, 128, 0.48, false, true},
+               {kT128x128, 128, 128, 0.47, true, false},       {kT64x128, 64, 128, 0.34, true, false},
+               {kT64x64, 64, 64, 0.24, true, false}};
   const struct {
     W8A8Form f;
     int mb, nb;
@@ -467,8 +473,11 @@ W8A8Form w8a8_form(int M, int N, int K) {
       t = us;
     }
   };
-  for (const auto& s : tiles)
-    if (M > 16) consider(s.f, 3.0 + kt * s.us * rounds(s.rows, s.cols));
+  if (M > 16)
+    for (const auto& s : tiles) {
+      const double r = rounds(s.rows, s.cols);
+      if (r > 1 ? s.several : s.one) consider(s.f, 3.0 + kt * s.us * r);
+    }
   if (M <= kSmallMaxRows)
     for (const auto& s : small) {
       if (s.mb > 1 && M <= 8 * s.mb) continue;  // half the row blocks hold as many rows
@@ -493,7 +502,9 @@ hipError_t launch_w8a8(const W8A8Args& a, hipStream_t stream) {
     case kT64x64: return launch_tile<2, 2, 2, 2, 4>(a, stream);
     case kT64x128: return launch_tile<2, 2, 2, 4, 4>(a, stream);
     case kT128x128: return launch_tile<2, 4, 4, 2, 4>(a, stream);
+    case kT128x128Shared: return launch_tile<2, 4, 4, 2, 2>(a, stream);
     case kT128x192: return launch_tile<2, 4, 4, 3, 3>(a, stream);
+    case kT128x192Shared: return launch_tile<2, 4, 4, 3, 2>(a, stream);
     default: return launch_tile<4, 2, 4, 6, 2>(a, stream);
   }
 }
