@@ -158,11 +158,13 @@ __device__ __forceinline__ bool live_logit(float& v) {
 // A sigmoid's score is off by less than 3e-7 whatever the logit (the
 // exponential's part that grows with |z| falls as |z| exp(-|z|)), a softmax's
 // by 3e-6 of the largest score (exponentials, 22 additions deep, quotient), and
-// the bias and a group's sum round at the value's own size. A decision compares
-// two values, or two sums of two.
+// the bias' addition rounds at the choice value's own size. A group's sum of two
+// carries both summands' roundings, each of its summand's size however small
+// the sum is (biases of opposite sign), and its own. A decision compares two
+// values, or two sums of two.
 constexpr float kRtMarginSigmoid = 2e-6f;
 constexpr float kRtMarginSoftmax = 1.6e-5f;  // of the largest score
-constexpr float kRtMarginValue = 5e-7f;      // of the values' magnitude
+constexpr float kRtMarginValue = 5e-7f;      // of the values' (a sum: summands') magnitude
 
 template <typename S>
 __device__ __forceinline__ S exp_of(S x) {
@@ -360,8 +362,11 @@ __device__ __forceinline__ bool apart_by(float hi, float lo, float margin, float
 }
 
 // keep: a bit per expert of the lane, whether its group is kept. Returns false,
-// and no bits, where the last group kept is nearer than the margin to the first
-// one dropped (S = float). vals: the wave's LDS.
+// and no bits, where the groups kept and those dropped are not further apart than
+// their errors (S = float): a value between the last one kept and the first one
+// dropped has to lie outside every group's value +- half the margin. Any group
+// may be the one that reaches it, as each errs by its own summands' size. vals: the
+// wave's LDS.
 template <int P, typename S, typename Key>
 __device__ __forceinline__ bool keep_groups(const RouteArgs& a, Key (&key)[P], float margin, int lane,
                                             Key* vals, uint32_t& keep) {
@@ -398,10 +403,22 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs& a, Key (&key)[P], f
     const S ov = lane_of(value, q * lg);
     place += ov > value || (ov == value && g > q);
   }
-  if (sizeof(S) == 4 && a.groups_kept < a.groups) {
-    const S low = lane_of(value, __builtin_ctzll(__ballot(place == a.groups_kept - 1)));
-    const S high = lane_of(value, __builtin_ctzll(__ballot(place == a.groups_kept)));
-    if (high > none && !apart_by(low, high, margin, kRtMarginValue)) return false;
+  if constexpr (sizeof(S) == 4) {
+    if (a.groups_kept < a.groups) {
+      const S low = lane_of(value, __builtin_ctzll(__ballot(place == a.groups_kept - 1)));
+      const S high = lane_of(value, __builtin_ctzll(__ballot(place == a.groups_kept)));
+      if (high > none) {
+        // half the margin a side: 4.2 half steps of fp32 of the summands' size; a
+        // summand's rounding, the sum's and that of value +- error are 3. Infinite
+        // sums fail either comparison.
+        S size = t1 ? __builtin_fabsf(value_of(t1)) : 0.f;
+        if (a.group_top == 2 && t2) size += __builtin_fabsf(value_of(t2));
+        const S error = 0.5f * (margin + kRtMarginValue * size);
+        const S between = 0.5f * low + 0.5f * high;
+        const bool clear = place < a.groups_kept ? value - error > between : value + error < between;
+        if (__any(g < a.groups && !clear)) return false;
+      }
+    }
   }
   const bool in = place < a.groups_kept;
   if (a.group_whole) {
