@@ -171,6 +171,8 @@ hipError_t launch_small(const W8A8Args& a, hipStream_t stream) {
   const int NCB = (a.N + 15) / 16;
   const size_t lds = static_cast<size_t>(WAVES) * MB * 1024 * (XS && NB < 2 ? 2 : NB);
   int MT = (a.M + 16 * MB - 1) / (16 * MB);
+  const long long blocks = static_cast<long long>((NCB + NB - 1) / NB) * MT;
+  if (blocks * 64 * WAVES > 0xFFFFFFFFLL) return hipErrorNotSupported;
   // read in operand order there is one row tile
   const void* fn = MT == 1 ? reinterpret_cast<const void*>(&w8a8_small_kernel<MB, NB, WAVES, XS, true>)
                            : reinterpret_cast<const void*>(&w8a8_small_kernel<MB, NB, WAVES, XS, !XS>);
@@ -181,7 +183,7 @@ hipError_t launch_small(const W8A8Args& a, hipStream_t stream) {
   }
   W8A8Args args = a;
   void* kargs[] = {&args, &MT};
-  return hipLaunchKernel(fn, dim3((NCB + NB - 1) / NB * MT), dim3(64 * WAVES), kargs, lds, stream);
+  return hipLaunchKernel(fn, dim3(static_cast<unsigned>(blocks)), dim3(64 * WAVES), kargs, lds, stream);
 }
 
 // -------------------------------------------------------------- many rows
