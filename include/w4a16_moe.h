@@ -144,7 +144,7 @@ int w4a16_gemm_experts(const void* x, const void* qweight, const void* scales, v
  *   y : device bf16 [T * top_k][N]; ids, weights : device int32 / f32 [T][top_k]
  *   base : device bf16 [T][N], or NULL for 0; out : device bf16 [T][N], may be
  *   base itself, otherwise overlaps no input. y, base, out 16-byte aligned.
- * Supported: T >= 0, N >= 1, 1 <= top_k <= W4A16_ROUTE_MAX_TOP_K,
+ * Supported: T >= 0, 1 <= N <= 2^31 - 8, 1 <= top_k <= W4A16_ROUTE_MAX_TOP_K,
  * T * top_k <= 2^30. T == 0 launches nothing.
  */
 int w4a16_moe_combine(const void* y, const int32_t* ids, const float* weights, const void* base,

@@ -12,6 +12,7 @@ namespace {
 
 constexpr long long kMaxSlots = 1LL << 30;
 constexpr long long kMaxRoutedSlots = 1LL << 26;
+constexpr int kMaxCombineColumns = 0x7FFFFFF8;   // rounded up to 8 still an int
 constexpr long long kMaxBuffer = 0xFFFFFE00LL;  // bytes a 32-bit buffer resource may span
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -119,7 +120,8 @@ int w4a16_moe_combine(const void* y, const int32_t* ids, const float* weights, c
   if (T < 0 || N < 0 || top_k < 1 || top_k > W4A16_ROUTE_MAX_TOP_K) return W4A16_ERR_INVALID_ARG;
   if (T == 0) return W4A16_OK;
   if (!y || !ids || !weights || !out) return W4A16_ERR_INVALID_ARG;
-  if (N < 1 || static_cast<long long>(T) * top_k > kMaxSlots) return W4A16_ERR_UNSUPPORTED;
+  if (N < 1 || N > kMaxCombineColumns || static_cast<long long>(T) * top_k > kMaxSlots)
+    return W4A16_ERR_UNSUPPORTED;
   if (!aligned(y, 16) || !aligned(base, 16) || !aligned(out, 16) || !aligned(ids, 4) ||
       !aligned(weights, 4))
     return W4A16_ERR_MISALIGNED;
