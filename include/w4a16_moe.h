@@ -126,7 +126,9 @@ typedef enum {
  *   rows, offsets : as w4a16_moe_route writes them, for `slots` = T * top_k
  * Rows of y whose slot is in no list are left as they are. Entries of the
  * lists outside 0 .. slots - 1 (and offsets outside 0 .. slots) are ignored;
- * a slot that is listed twice gives an unspecified one of its results.
+ * where a slot is listed twice, each value of its row is an unspecified one of
+ * its results. Offsets that do not ascend list slots several times: a row of y
+ * may then also be left as it is.
  * Supported: 0 <= slots <= 2^30, 1 <= experts <= W4A16_ROUTE_MAX_EXPERTS,
  * x_div >= 1, N >= 1, group in {32, 64, 128, 256}, K % group == 0; SWIGLU needs
  * N % 32 == 0; x and one expert's packed weights below 4 GB each, and a grid

@@ -48,8 +48,9 @@ struct Place {
 
 // Expert and row tile of unit `u` of all experts' (row tile, column tile)
 // units, NT column tiles each; TM rows per row tile. Offsets out of range are
-// clamped, so that a bad list cannot lead outside the buffers. `total` is the
-// number of units.
+// clamped, so that a bad list cannot lead outside the buffers; and the tiles are
+// counted up to the grid's (`most`, at most 2^24: 64 lanes' counts fit an int),
+// since offsets that do not ascend can list the slots E / 2 times over.
 template <int TM>
 struct TileMap {
   static constexpr int kHeld = 4;  // experts per lane held in registers
@@ -79,7 +80,7 @@ struct TileMap {
       }
     }
   }
-  __device__ __forceinline__ void setup(const int* offsets, int E_, int slots_) {
+  __device__ __forceinline__ void setup(const int* offsets, int E_, int slots_, int most) {
     off = offsets;
     E = E_;
     slots = slots_;
@@ -91,6 +92,7 @@ struct TileMap {
     }
     sum = 0;
     each([&](int, int lo, int hi) { sum += tiles_of(lo, hi); });
+    sum = min(sum, most);
     int s = sum;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -98,7 +100,7 @@ struct TileMap {
       if (lane >= o) s += v;
     }
     excl = s - sum;
-    total_tiles = __builtin_amdgcn_readlane(s, 63);
+    total_tiles = min(__builtin_amdgcn_readlane(s, 63), most);
   }
   // The place of unit u < total_tiles * NT, and its column tile.
   __device__ __forceinline__ Place find(int u, int NT, int& nt) const {
@@ -143,13 +145,13 @@ __device__ __forceinline__ float swiglu(float gate, float up) {
 // row piece, and turned into the MFMA operand arrangement through a
 // wave-private LDS area (lg_slot: free of bank conflicts).
 template <int GS, int MB, int NB, int WAVES, int P4, int P16, bool XS, bool ACT>
-__global__ __launch_bounds__(64 * WAVES) void experts_small_kernel(const ExpertsArgs a, int NT) {
+__global__ __launch_bounds__(64 * WAVES) void experts_small_kernel(const ExpertsArgs a, int NT, int row_tiles) {
   constexpr int WPL = GS / 32;
   constexpr int TM = 16 * MB;
   static_assert(!XS || GS == 128, "coalesced staging: group 128");
   static_assert(!ACT || NB % 2 == 0, "gate and up blocks in pairs");
   TileMap<TM> map;
-  map.setup(a.offsets, a.E, a.slots);
+  map.setup(a.offsets, a.E, a.slots, row_tiles);
   const int total = map.total_tiles * NT;
   if (static_cast<int>(blockIdx.x) >= total) return;
   int nt;
@@ -354,8 +356,8 @@ hipError_t launch_small_t(const ExpertsArgs& a, hipStream_t stream) {
   constexpr int TM = 16 * MB;
   const int NCB = (a.N + 15) / 16;
   int NT = ACT ? (NCB / 2 + NB / 2 - 1) / (NB / 2) : (NCB + NB - 1) / NB;
-  const long long row_tiles = a.slots / TM + (a.slots < a.E ? a.slots : a.E);
-  const long long blocks = row_tiles * NT;
+  int row_tiles = a.slots / TM + (a.slots < a.E ? a.slots : a.E);
+  const long long blocks = static_cast<long long>(row_tiles) * NT;
   if (blocks * 64 * WAVES > 0xFFFFFFFFLL) return hipErrorNotSupported;
   size_t lds = static_cast<size_t>(WAVES) * MB * NB * 1024;
   if (XS) lds += static_cast<size_t>(WAVES) * MB * 16 * 256;
@@ -366,7 +368,7 @@ hipError_t launch_small_t(const ExpertsArgs& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   ExpertsArgs args = a;
-  void* kargs[] = {&args, &NT};
+  void* kargs[] = {&args, &NT, &row_tiles};
   return hipLaunchKernel(fn, dim3(static_cast<unsigned>(blocks)), dim3(64 * WAVES), kargs, lds, stream);
 }
 
@@ -443,12 +445,12 @@ __device__ __forceinline__ void expert_tile(const ExpertsArgs& a, unsigned char*
 // MB: the most row blocks of a tile; the last tile of an expert takes the
 // smallest of 2, 4, 8 row blocks that hold its rows.
 template <int GS, int MB, bool ACT>
-__global__ __launch_bounds__(kLgThreads, 1) void experts_tile_kernel(const ExpertsArgs a, int NT) {
+__global__ __launch_bounds__(kLgThreads, 1) void experts_tile_kernel(const ExpertsArgs a, int NT, int row_tiles) {
   constexpr int Rows = MB * 16;
   extern __shared__ __attribute__((aligned(16))) unsigned char ex_tile_lds[];
   __shared__ int slot_of[Rows];
   TileMap<Rows> map;
-  map.setup(a.offsets, a.E, a.slots);
+  map.setup(a.offsets, a.E, a.slots, row_tiles);
   const int total = map.total_tiles * NT;
   if (static_cast<int>(blockIdx.x) >= total) return;
   int nt;
@@ -477,8 +479,8 @@ hipError_t launch_tile_t(const ExpertsArgs& a, hipStream_t stream) {
   constexpr size_t Lds = LgCfg<GS, MB>::Lds > Out ? LgCfg<GS, MB>::Lds : Out;
   const int NCB = (a.N + 15) / 16;
   int NT = ACT ? (NCB / 2 + kLgWaves - 1) / kLgWaves : (NCB + kLgBlocks - 1) / kLgBlocks;
-  const long long row_tiles = a.slots / Rows + (a.slots < a.E ? a.slots : a.E);
-  const long long blocks = row_tiles * NT;
+  int row_tiles = a.slots / Rows + (a.slots < a.E ? a.slots : a.E);
+  const long long blocks = static_cast<long long>(row_tiles) * NT;
   if (blocks * kLgThreads > 0xFFFFFFFFLL) return hipErrorNotSupported;
   const void* fn = reinterpret_cast<const void*>(&experts_tile_kernel<GS, MB, ACT>);
   if (Lds > 64 * 1024) {
@@ -487,7 +489,7 @@ hipError_t launch_tile_t(const ExpertsArgs& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   ExpertsArgs args = a;
-  void* kargs[] = {&args, &NT};
+  void* kargs[] = {&args, &NT, &row_tiles};
   return hipLaunchKernel(fn, dim3(static_cast<unsigned>(blocks)), dim3(kLgThreads), kargs, Lds, stream);
 }
 
