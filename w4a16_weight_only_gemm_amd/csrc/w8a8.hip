@@ -221,7 +221,10 @@ __device__ __forceinline__ rsrc4 raw_rsrc(const void* base, uint32_t bytes) {
 // lds .. lds + 1023 (lane l's at 16 l), without passing through registers.
 // In inline assembly because the compiler, which cannot tell these LDS bytes
 // from others, would wait for every such copy before the next LDS read; the
-// loops that use it hold every wait themselves.
+// loops that use it hold every wait themselves. M0 is named as written, of which
+// the compiler warns, as it gives M0 to no value of its own.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy_to_lds(uint32_t lds, uint32_t voff, rsrc4 r) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
@@ -229,8 +232,9 @@ __device__ __forceinline__ void copy_to_lds(uint32_t lds, uint32_t voff, rsrc4 r
       "buffer_load_dwordx4 %1, %2, 0 offen lds"
       :
       : "s"(lds), "v"(voff), "s"(r)
-      : "memory");
+      : "m0", "memory");
 }
+#pragma clang diagnostic pop
 
 // Waits until at most N of the wave's loads are on their way.
 template <int N>
