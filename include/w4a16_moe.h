@@ -73,7 +73,11 @@ size_t w4a16_moe_route_workspace_bytes(int T, int experts);
  * is the sum of its group_top largest v (fewer where fewer are there), and
  * only the groups_kept groups of largest value are chosen from. The top_k
  * largest v are the token's experts, in descending order; equal values go to
- * the lowest index, for groups too. The weight of a choice is its score
+ * the lowest index, for groups too. With bias NULL and groups = 1 the logits
+ * themselves are compared, which scores grow with: logits whose scores are
+ * equal in 64 bits (sigmoids of 37 and more are 1; a softmax's scores 746 below
+ * the largest are 0) are still told apart there, and are equal values with a
+ * bias, be it of zeros, or groups. The weight of a choice is its score
  * (without bias), divided by the sum of the token's chosen scores if
  * `renormalize` is set, times scale. Scores, choice values and sums are held
  * in 64 bits, so that which expert is chosen does not depend on rounding.
