@@ -136,8 +136,8 @@ typedef enum {
  * Supported: 0 <= slots <= 2^30, 1 <= experts <= W4A16_ROUTE_MAX_EXPERTS,
  * x_div >= 1, N >= 1, group in {32, 64, 128, 256}, K % group == 0; SWIGLU needs
  * N % 32 == 0; x and one expert's packed weights below 4 GB each, and a grid
- * of at most 2^32 threads (else W4A16_ERR_UNSUPPORTED). x, qweight, scales, y 16-byte aligned, the lists
- * 4-byte. slots == 0 launches nothing. y must not overlap any input.
+ * of fewer than 2^32 threads (else W4A16_ERR_UNSUPPORTED). x, qweight, scales, y
+ * 16-byte aligned, the lists 4-byte. slots == 0 launches nothing. y must not overlap any input.
  */
 int w4a16_gemm_experts(const void* x, const void* qweight, const void* scales, void* y,
                        const int32_t* rows, const int32_t* offsets, int slots, int experts,
@@ -163,7 +163,9 @@ int w4a16_moe_combine(const void* y, const int32_t* ids, const float* weights, c
  *     y[m][n] = sx[m] * sw[n] * sum_k xq[m][k] * q[n][k]
  *
  * the sum exact in int32, the scaling in fp32, y rounded to bf16 (nearest
- * even).
+ * even). sx[m] * sw[n] is formed first: where that product is not a normal fp32
+ * number (below 2^-126, or past the largest), y has its loss of digits or its
+ * infinity.
  *
  * Packed weights: columns in blocks of 16 (the last padded with zero codes), k
  * in steps of 64 (the last padded with zero codes); int8
@@ -185,8 +187,9 @@ int w8a8_pack(const int8_t* q, int8_t* qweight_out, int N, int K);
  *   qweight : device copy of what w8a8_pack wrote; sw : device f32 [N]
  *   y : device bf16 [M][N], overlapping no input
  * Supported: M >= 0, N >= 1, 16 <= K <= 131072 (so that no int32 sum can
- * overflow), K % 16 == 0, packed weights below 4 GB, a grid of at most 2^32
- * threads; other shapes return W4A16_ERR_UNSUPPORTED. Every pointer 16-byte aligned (sw and sx: 4-byte).
+ * overflow), K % 16 == 0, packed weights below 4 GB, a grid of fewer than 2^32
+ * threads; other shapes return W4A16_ERR_UNSUPPORTED. Every pointer 16-byte
+ * aligned (sw and sx: 4-byte).
  * M == 0 launches nothing. Needs no workspace.
  */
 int w8a8_gemm(const void* xq, const float* sx, const void* qweight, const float* sw, void* y,

@@ -20,8 +20,8 @@
 //    first weights need only the offsets and start beside it).
 //  * otherwise experts_tile_kernel, the R x 256 MFMA tile engine of the dense
 //    product with its rows gathered: 32-row tiles, bound by HBM while the
-//    experts have few rows each (5.6 TB/s at 37 tokens of 8 experts out of
-//    128), 128-row tiles, bound by LDS reads and MFMA, when they have many.
+//    experts have few rows each (4.6 TB/s at 37 tokens of 8 experts out of
+//    128, of which 93 have rows), 128-row tiles, bound by LDS reads and MFMA, when they have many.
 //
 // With SwiGLU a workgroup owns the same columns of the gate half and of the
 // up half (its column blocks come in such pairs), so the activation is formed
@@ -504,11 +504,23 @@ hipError_t launch_tile_t(const ExpertsArgs& a, hipStream_t stream) {
 // For instance (us, few rows against 32-row tiles, 128 experts): 2048 x 5120 at
 // 1 token 11.2 / 31.9, at 16 86 / 84, at 64 140 / 113; 5120 x 1024 at 1 token
 // 12.0 / 10.5, at 64 136 / 68. While there is at most one workgroup per compute
-// unit, few rows takes 64 columns and 8 waves (2048 x 5120 at 1 token: 10.1).
+// unit, few rows takes 64 columns and 8 waves (2048 x 5120 at 1 token: 11.0
+// against 11.7). With 8 waves a compute unit has enough on the way with one
+// group per wave: 1, 2, 3 and 5 ahead 11.0, 11.1, 12.1, 13.5; 1536 x 2048 6.8,
+// 7.3, 8.0, 8.7. With 4 waves 1, 2, 4 and 6 ahead: 12.2, 11.5, 11.7, 13.1; 2048 x
+// 5120 at 4 tokens 35.1, 33.3, 33.0, 37.0.
 // 128-row tiles from 100 rows per expert on with two workgroups per compute
-// unit or more (32-row against 128-row: 2048 x 5120, 128 experts, mean 64: 299
-// / 344, 128: 498 / 479, 256: 915 / 810; 8 experts of 256 rows: 54 / 75).
-// Group 256 has no tile engine.
+// unit or more (32-row against 128-row: 2048 x 5120, 128 experts, mean 64: 246
+// / 292, 128: 437 / 438, 256: 915 / 810; 8 experts of 256 rows: 55 / 74).
+// Over 180 shapes (the five N x K, 8, 32 and 128 experts, 1 to 2048 tokens, even
+// spread, weights from HBM) the form taken needs 1.02 times the fastest in the
+// mean and 1.35 at worst (2048 x 768, 16 tokens of 8 experts: 8.9 against 6.6).
+// 128-row tiles are ahead below that bound in places: 8 experts of 512 rows 104 /
+// 83, group 32, 1344 x 2688, 40 experts of 200 rows 145 / 120.
+// Group 256 has no tile engine; 16 rows a workgroup, from 12 rows per expert on
+// 32, which reads the weights half as often but is behind where measured (16 rows
+// each, 16 rows x 64 columns against 32 x 32: 2048 x 5120 347 / 394, 5120 x 1024
+// 238 / 385).
 template <int GS, bool ACT>
 hipError_t launch_experts_t(const ExpertsArgs& a, hipStream_t stream) {
   const double mean = static_cast<double>(a.slots) / a.E;
@@ -526,7 +538,6 @@ hipError_t launch_experts_t(const ExpertsArgs& a, hipStream_t stream) {
       return launch_tile_t<GS, 2, ACT>(a, stream);
     }
   } else {
-    // 16 against 32 rows a workgroup where most tiles would be past 16
     if (mean >= 12) return launch_small_t<GS, 2, 2, 8, 1, 1, ACT>(a, stream);
   }
   if (active * std::ceil(blocks / 4) <= kModelCUs) return launch_small_t<GS, 1, 4, 8, 1, 1, ACT>(a, stream);

@@ -15,9 +15,11 @@
 //    64 bits: in fp32 two experts a few 1e-8 apart could swap places. They are
 //    first formed in fp32; choices nearer than a margin that covers every fp32
 //    rounding on the way are formed in fp64, a lane each, and ordered by that. Of
-//    groups only the last one kept and the first one dropped have to be apart;
-//    where they are not, the token's groups are formed again in fp64. Either
-//    happens to one token of some hundreds with a router of 256 experts.
+//    groups only those kept and those dropped have to be apart;
+//    where they are not, the token's groups are formed again in fp64. With 256
+//    experts in 8 groups, sigmoid scores of normal logits (1.5) and biases (0.05),
+//    choices are near for one token in 450, groups for one in 11,000 (this rule
+//    over 200,000 tokens).
 // The weights need the scores of the chosen experts only, in fp64: a thread per
 // slot, after the workgroup's tokens are chosen (softmax without renormalisation
 // also sums over all experts, in fp64).

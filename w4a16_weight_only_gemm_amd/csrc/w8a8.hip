@@ -441,9 +441,9 @@ hipError_t launch_tile(const W8A8Args& a, hipStream_t stream) {
 // 128 x 128 and 128 x 192 hold more buffers while there is one round, and from
 // two on two buffers, so that two workgroups share a compute unit. Measured on N
 // x K = 7168 x 5120, 5120 x 6144, 34816 x 5120, 5120 x 17408, their eighths, 12000
-// x 4096, 2756 x 10368, 21968 x 1408, 710 x 17408 and 1500 x 704 at M = 17 to 4096
-// with every form: the one chosen takes 1.004 times the fastest measured in the
-// mean and at most 1.11. For instance (us): 5120 x 17408, M = 64: 2 x 3 blocks
+// x 4096, 2756 x 10368, 21968 x 1408, 710 x 17408 and 1500 x 704 at M = 1 to 4096
+// with every form (214 shapes): the one chosen takes 1.003 times the fastest
+// measured in the mean and at most 1.13. For instance (us): 5120 x 17408, M = 64: 2 x 3 blocks
 // 27.1, 2 x 4 31.3; M = 256: 64 x 128 55, 64 x 64 63, 128 x 128 72; 34816 x 5120, M
 // = 64: 128 x 192 37, 64 x 128 50, 2 x 4 blocks 61; M = 512: 128 x 192 98, 256 x
 // 192 103; M = 1024: 175, 155; 7168 x 5120, M = 2048: 128 x 192 with two buffers
