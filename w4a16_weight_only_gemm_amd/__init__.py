@@ -466,3 +466,4 @@ def w4a16_read_probe(buf, nbytes: int, sink, sink_bytes: int = READ_PROBE_SINK_B
 
 
 from ._moe import *  # noqa: E402,F401,F403  (the operators of include/w4a16_moe.h)
+from ._layer import *  # noqa: E402,F401,F403  (the operators of include/w4a16_layer.h)

@@ -40,6 +40,18 @@ __device__ __forceinline__ void store_piece(gptr<uint16_t> y, u32x4 v, int left)
   }
 }
 
+// Eight bf16 of a row, or the first `left` of them (zeros behind), from any even
+// address.
+__device__ __forceinline__ u32x4 load_piece(gptr<const uint16_t> x, int left) {
+  typedef uint32_t piece __attribute__((ext_vector_type(4), aligned(2)));
+  if (left >= 8) return *reinterpret_cast<gptr<const piece>>(x);
+  u32x4 v = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (i < left) v[i / 2] |= static_cast<uint32_t>(x[i]) << (16 * (i % 2));
+  return v;
+}
+
 // A value read through the constant address space: the memory must not be
 // written while the kernel runs (a plan's problem table), and a uniform
 // address then becomes a scalar load into SGPRs.
