@@ -9,19 +9,21 @@
 // wave needs of the activations does not depend on the expert.
 //  * router_kernel: a workgroup per expert, products and sums in fp64 (a bf16 by f32
 //    product is exact there), so that the choice does not depend on an order of
-//    additions. It also clears the counters of the last kernel.
-//  * gate_up_kernel: every workgroup chooses the experts itself, from the logits
-//    (E doubles a token), and lists those that are active; a wave owns a range of K
-//    and holds its tokens' activations of that range in registers for as long as
-//    the workgroup lives, while the weights of one (expert, 16 gate and 16 up
-//    columns) after the other stream by, a whole task ahead. The waves' sums meet
-//    in LDS, where SwiGLU is formed.
-//  * down_kernel: the active experts' k ranges laid end to end are one long sum for
-//    every 16 columns of the output, each expert's part weighted by its tokens'
-//    weights on the way. The (16 columns, expert, k) units are dealt out evenly to
-//    the workgroups; columns that lie with several are joined through the
-//    workspace by the last to arrive, in the order of the workgroups, so results
-//    do not depend on timing.
+//    additions. It also clears the counters of the other kernel.
+//  * experts_kernel, one workgroup per compute unit:
+//    - every workgroup chooses the experts itself, from the logits, and lists those
+//      that are active;
+//    - gate and up: a wave owns a range of K and holds its tokens' activations of
+//      that range in registers, while the weights of one (expert, 16 gate and 16 up
+//      columns) after the other stream by, a whole task ahead. The waves' sums meet
+//      in LDS, where SwiGLU is formed;
+//    - down: the active experts' k ranges laid end to end are one long sum for every
+//      16 columns of the output, each expert's part weighted by its tokens' weights on
+//      the way. A workgroup takes a few column blocks of a part of it; the parts are
+//      added by the last workgroup to finish one, in their order, so results do not
+//      depend on timing.
+//    Between the two every workgroup waits for all inner rows, its first weights of
+//    down on their way meanwhile.
 // Bound by HBM from a few tokens on; at one token by the launches and by the chain
 // logits, choice, first weights.
 #include <hip/hip_runtime.h>
@@ -42,8 +44,9 @@ constexpr int kMlTokens = W4A16_MOE_LAYER_MAX_TOKENS;
 constexpr int kMlMaxK = W4A16_ROUTE_MAX_TOP_K;
 constexpr int kMlWaves = 8;
 constexpr int kMlThreads = 64 * kMlWaves;
-constexpr int kMlMaxGrid = 512;        // workgroups of the product kernels
-constexpr int kMlRouterThreads = 256;
+constexpr int kMlMaxNB = 8;            // column blocks of a workgroup of down_kernel
+constexpr int kMlInnerBytes = 32 * 1024;  // inner rows that are held in LDS, at most
+constexpr int kMlRouterThreads = 1024;  // at most
 constexpr int kMlPartFloats = 256;     // a 16 x 16 part
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
@@ -54,10 +57,13 @@ struct MlSpace {
 };
 MlSpace ml_space(int T, int E, int top_k, int H, int I) {
   MlSpace s;
-  s.logits = up256((static_cast<size_t>(H) + 15) / 16 * 4);  // the counters are in front
+  // the counters are in front
+  s.logits = up256((static_cast<size_t>(H) + 15) / 16 * 4);
   s.h = s.logits + up256(static_cast<size_t>(T) * E * 8);
   s.parts = s.h + up256(static_cast<size_t>(T) * top_k * I * 2);
-  s.total = s.parts + static_cast<size_t>(kMlMaxGrid) * 2 * kMlPartFloats * 4;
+  // 16 x 16 floats for every column block of every split: at most kModelCUs splits
+  // of kMlMaxNB blocks (one split needs none)
+  s.total = s.parts + static_cast<size_t>(kModelCUs) * kMlMaxNB * kMlPartFloats * 4;
   return s;
 }
 
@@ -76,8 +82,8 @@ struct MlArgs {
   float* weights;
   double* logits;   // [T][E]
   uint16_t* h;      // bf16 [T][top_k][I]
-  float* parts;     // [workgroups][2][16][16]
-  int* counters;    // [H / 16]
+  float* parts;     // [columns][splits][blocks][16][16]
+  int* counters;    // [H / 16]: parts that are there of every group of columns
   int T, E, top_k, H, I;
   int sigmoid, groups, groups_kept, group_top, renormalize;
   float scale;
@@ -93,95 +99,155 @@ __device__ __forceinline__ void wave_sync() {
 
 // ------------------------------------------------------------------ router
 
-template <bool HALF>
+// TB: tokens it has registers for, T rounded up to a power of two. The row's 16-byte
+// pieces go round the threads.
+template <bool HALF, int TB>
 __global__ __launch_bounds__(kMlRouterThreads) void router_kernel(const MlArgs a) {
-  __shared__ double part[kMlRouterThreads / 64][kMlTokens];
+  __shared__ double part[kMlRouterThreads / 64][TB];
   const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int i = blockIdx.x * kMlRouterThreads + tid; i < (a.H + 15) / 16; i += gridDim.x * kMlRouterThreads)
+  const int threads = blockDim.x;
+  for (int i = blockIdx.x * threads + tid; i < (a.H + 15) / 16; i += gridDim.x * threads)
     to_global(a.counters)[i] = 0;
-  double acc[kMlTokens];
+  double acc[TB];
 #pragma unroll
-  for (int t = 0; t < kMlTokens; ++t) acc[t] = 0.0;
-  for (int c = tid * 8; c < a.H; c += kMlRouterThreads * 8) {
-    float w[8];
+  for (int t = 0; t < TB; ++t) acc[t] = 0.0;
+  for (int c = tid * 8; c < a.H; c += threads * 8) {
+    u32x4 x[TB];  // tokens past the last repeat it
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+      x[t] = *reinterpret_cast<gptr<const u32x4>>(to_global(a.x) + static_cast<size_t>(min(t, a.T - 1)) * a.H + c);
+    double w[8];
     if constexpr (HALF) {
       const u32x4 d = *reinterpret_cast<gptr<const u32x4>>(to_global(static_cast<const uint16_t*>(a.router)) +
                                                            static_cast<size_t>(e) * a.H + c);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        w[j] = __builtin_bit_cast(float, j % 2 ? d[j / 2] & 0xFFFF0000u : d[j / 2] << 16);
+        w[j] = static_cast<double>(__builtin_bit_cast(float, j % 2 ? d[j / 2] & 0xFFFF0000u : d[j / 2] << 16));
     } else {
       const gptr<const float> p = to_global(static_cast<const float*>(a.router)) + static_cast<size_t>(e) * a.H + c;
       const f32x4 lo = *reinterpret_cast<gptr<const f32x4>>(p), hi = *reinterpret_cast<gptr<const f32x4>>(p + 4);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = j < 4 ? lo[j % 4] : hi[j % 4];
+      for (int j = 0; j < 8; ++j) w[j] = static_cast<double>(j < 4 ? lo[j % 4] : hi[j % 4]);
     }
 #pragma unroll
-    for (int t = 0; t < kMlTokens; ++t) {
-      if (t >= a.T) continue;
-      const u32x4 d = *reinterpret_cast<gptr<const u32x4>>(to_global(a.x) + static_cast<size_t>(t) * a.H + c);
+    for (int t = 0; t < TB; ++t)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float xv = __builtin_bit_cast(float, j % 2 ? d[j / 2] & 0xFFFF0000u : d[j / 2] << 16);
-        acc[t] = __builtin_fma(static_cast<double>(xv), static_cast<double>(w[j]), acc[t]);
+        const float xv = __builtin_bit_cast(float, j % 2 ? x[t][j / 2] & 0xFFFF0000u : x[t][j / 2] << 16);
+        acc[t] = __builtin_fma(static_cast<double>(xv), w[j], acc[t]);
       }
-    }
   }
 #pragma unroll
-  for (int t = 0; t < kMlTokens; ++t) {
-    if (t >= a.T) continue;
+  for (int t = 0; t < TB; ++t) {
     const double s = wave_sum_of(acc[t]);
     if (lane == 0) part[wave][t] = s;
   }
   __syncthreads();
   if (tid < a.T) {
     double s = part[0][tid];
-#pragma unroll
-    for (int w = 1; w < kMlRouterThreads / 64; ++w) s += part[w][tid];
+    for (int w = 1; w < threads / 64; ++w) s += part[w][tid];
     to_global(a.logits)[static_cast<size_t>(tid) * a.E + e] = s;
   }
 }
 
 // ------------------------------------------------------------------ choice
 
-// One wave chooses one token's experts: the rule of w4a16_moe_route in fp64
-// throughout. scratch: E keys of LDS.
+// The wave's largest key and, of equal ones, the lowest expert (-1: no key is left),
+// taken out of the keys. Keys nearly always differ in their high words, so the low
+// ones are compared only among those that share the largest.
 template <int P>
-__device__ __forceinline__ void choose(const MlArgs& a, int t, uint64_t* scratch, int lane, short* ids, float* weights) {
-  const bool here = !a.live || a.live[t] != 0;
-  const gptr<const double> logits = to_global(a.logits) + static_cast<size_t>(t) * a.E;
-  auto finite = [](double v) { return (v > DBL_MAX ? DBL_MAX : v) + 0.0; };  // and -0 is 0
+__device__ __forceinline__ int take_one(uint32_t (&hi)[P], uint32_t (&lo)[P], int lane) {
+  uint32_t best = hi[0];
+#pragma unroll
+  for (int i = 1; i < P; ++i) best = hi[i] > best ? hi[i] : best;
+  const uint32_t top = wave_max_of(best);
+  if (top == 0) return -1;  // keys of numbers have a high word
+  int many = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) many += __popcll(__ballot(hi[i] == top));
+  uint32_t low = 0;
+  if (many > 1) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) low = hi[i] == top && lo[i] > low ? lo[i] : low;
+    low = wave_max_of(low);
+  }
+  int e = -1;
+#pragma unroll
+  for (int i = P - 1; i >= 0; --i) {
+    const uint64_t who = __ballot(hi[i] == top && (many == 1 || lo[i] == low));
+    if (who) e = i * 64 + __builtin_ctzll(who);
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    if (e == i * 64 + lane) hi[i] = 0;
+  return e;
+}
+
+// One token's experts by the rule of w4a16_moe_route, in fp64 throughout; a wave does
+// all of it, or several share the comparisons. P: experts per lane, expert i * 64 +
+// lane the i-th.
+template <int P>
+struct Choice {
+  const MlArgs& a;
+  int t, lane;
+  uint64_t* scratch;  // E keys of LDS, the wave's own
+  gptr<const double> logits;
   uint64_t key[P];  // of the logits, then of the choice values; 0: cannot be chosen
-  uint64_t m = 0;
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int e = i * 64 + lane;
-    const double v = e < a.E ? logits[e] : -__builtin_inf();
-    key[i] = here && v > -__builtin_inf() ? order_key(finite(v)) : 0;
-    m = key[i] > m ? key[i] : m;
+  double most, sum;
+
+  static __device__ __forceinline__ double finite(double v) { return (v > DBL_MAX ? DBL_MAX : v) + 0.0; }  // -0 is 0
+  __device__ __forceinline__ double score(double z) const {
+    return a.sigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - most) / sum;
   }
-  double most = 0.0, sum = 0.0;
-  if (!a.sigmoid) {
-    m = wave_max_of(m);
-    most = m ? value_of(m) : 0.0;
+
+  // beside: loads that may come behind the logits'
+  template <typename F>
+  __device__ __forceinline__ Choice(const MlArgs& args, int token, int lane_, uint64_t* scratch_, F beside)
+      : a(args), t(token), lane(lane_), scratch(scratch_), most(0.0), sum(1.0) {
+    logits = to_global(a.logits) + static_cast<size_t>(t) * a.E;
+    double z[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) z[i] = logits[min(i * 64 + lane, a.E - 1)];
+    __builtin_amdgcn_sched_barrier(0);
+    beside();
+    __builtin_amdgcn_sched_barrier(0);
+    const bool here = !a.live || a.live[t] != 0;
+    uint64_t m = 0;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      sum += key[i] ? exp(value_of(key[i]) - most) : 0.0;
-      __builtin_amdgcn_sched_barrier(0);  // one exponential's registers at a time
+      const bool open = here && i * 64 + lane < a.E && z[i] > -__builtin_inf();
+      key[i] = open ? order_key(finite(z[i])) : 0;
+      m = key[i] > m ? key[i] : m;
     }
-    sum = wave_sum_of(sum);
-  }
-  auto score = [&](double z) { return a.sigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - most) / sum; };
-  if (a.route_bias || a.groups > 1) {
+    const bool by_value = a.route_bias || a.groups > 1;
+    if (!a.sigmoid) {
+      m = wave_max_of(m);
+      most = m ? value_of(m) : 0.0;
+      // a sum over all experts divides every score: it matters unless experts are
+      // compared by their logits and scores are divided by their own sum
+      if (by_value || !a.renormalize) {
+        sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int e = i * 64 + lane;
-      const double bias = a.route_bias && e < a.E ? to_global(a.route_bias)[e] : 0.f;
-      if (key[i]) key[i] = order_key(score(value_of(key[i])) + bias + 0.0);
-      __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < P; ++i) {
+          sum += key[i] ? exp(value_of(key[i]) - most) : 0.0;
+          __builtin_amdgcn_sched_barrier(0);  // one exponential's registers at a time
+        }
+        sum = wave_sum_of(sum);
+      }
     }
+    if (by_value) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const int e = i * 64 + lane;
+        const double bias = a.route_bias && e < a.E ? to_global(a.route_bias)[e] : 0.f;
+        if (key[i]) key[i] = order_key(score(value_of(key[i])) + bias + 0.0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (a.groups > 1) keep_groups();
   }
-  if (a.groups > 1) {
+
+  __device__ __forceinline__ void keep_groups() {
     // lane g looks at group g: its largest value, or the sum of its two largest
 #pragma unroll
     for (int i = 0; i < P; ++i)
@@ -211,16 +277,130 @@ __device__ __forceinline__ void choose(const MlArgs& a, int t, uint64_t* scratch
     }
     wave_sync();
   }
-  const int id = take<P, false>(key, a.top_k, lane);
-  double w = id >= 0 ? score(finite(logits[id])) : 0.0;
-  if (a.renormalize) {
-    const double s = wave_sum_of(w);
-    w = s > 0.0 ? w / s : 0.0;
+
+  // How many of the experts of the part-th of `parts` ranges have a larger high word,
+  // for each of the lane's.
+  __device__ __forceinline__ void count_larger(int part, int parts, int (&larger)[P]) const {
+    uint32_t* const words = reinterpret_cast<uint32_t*>(scratch);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      if (i * 64 + lane < (a.E + 3) / 4 * 4) words[i * 64 + lane] = key[i] >> 32;  // 0 past the last
+      larger[i] = 0;
+    }
+    wave_sync();
+    const int quads = (a.E + 3) / 4;
+    for (int q = quads * part / parts; q < quads * (part + 1) / parts; ++q) {
+      const u32x4 other = reinterpret_cast<const u32x4*>(words)[q];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < P; ++i) larger[i] += other[j] > static_cast<uint32_t>(key[i] >> 32);
+    }
+    wave_sync();
   }
-  if (lane < a.top_k) {
-    ids[lane] = static_cast<short>(id);
-    weights[lane] = static_cast<float>(w * a.scale);
+
+  // The lane's choice (lane j the j-th, -1 past the last) from the counts over all
+  // experts. Keys that share a high word leave a place empty or make too many: then,
+  // and where there are no counts, one choice after the other is taken.
+  __device__ __forceinline__ int order(const int* larger) {
+    int live = 0, few = 0;
+    bool counted = larger != nullptr;
+    if (counted) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        live += __popcll(__ballot(key[i] != 0));
+        few += __popcll(__ballot(key[i] != 0 && larger[i] < a.top_k));
+      }
+      const int want = min(live, a.top_k);
+      int* const places = reinterpret_cast<int*>(scratch);
+      if (lane < a.top_k) places[lane] = -1;
+      wave_sync();
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (key[i] && larger[i] < a.top_k) places[larger[i]] = i * 64 + lane;
+      wave_sync();
+      const int id = lane < a.top_k ? places[lane] : -1;
+      wave_sync();
+      if (few == want && __popcll(__ballot(id >= 0)) == want) return id;
+    }
+    uint32_t hi[P], lo[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      hi[i] = static_cast<uint32_t>(key[i] >> 32);
+      lo[i] = static_cast<uint32_t>(key[i]);
+    }
+    int id = -1;
+    for (int j = 0; j < a.top_k; ++j) {
+      const int e = take_one<P>(hi, lo, lane);
+      if (e < 0) break;
+      if (lane == j) id = e;
+    }
+    return id;
   }
+
+  // ids and weights of the token; `write`: to the caller's arrays too.
+  __device__ __forceinline__ void finish(int id, short* ids, float* weights, bool write) const {
+    double w = id >= 0 ? score(finite(logits[id])) : 0.0;
+    if (a.renormalize) {
+      const double s = wave_sum_of(w);
+      w = s > 0.0 ? w / s : 0.0;
+    }
+    if (lane < a.top_k) {
+      ids[lane] = static_cast<short>(id);
+      weights[lane] = static_cast<float>(w * a.scale);
+      if (write) {
+        to_global(a.ids)[t * a.top_k + lane] = id;
+        to_global(a.weights)[t * a.top_k + lane] = static_cast<float>(w * a.scale);
+      }
+    }
+  }
+};
+
+// All tokens' experts, into ids[token][kMlMaxK] and chosen. Every thread. counts: E ints
+// of LDS for every token while a token has several waves. Up to 4 tokens share the waves
+// evenly, so that a token's E^2 comparisons are spread over 8 to 2 of them; with more
+// tokens a wave has tokens of its own, and compares where that is less work than
+// top_k rounds over the wave (128 experts, 8 choices: 0.9 against 1.8 us a token; 256:
+// twice the rounds).
+// beside: loads of every wave that are wanted behind the choice.
+template <int P, typename F>
+__device__ __forceinline__ void choose_all(const MlArgs& a, uint64_t* scratch, int* counts, short (*ids)[kMlMaxK],
+                                           float (*chosen)[kMlMaxK], bool write, F beside) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  scratch += static_cast<size_t>(wave) * ((a.E + 3) / 4 * 4);
+  if (a.T <= 4 && P <= 4) {
+    const int per = a.T == 1 ? 8 : a.T == 2 ? 4 : 2;  // waves a token
+    const int t = min(wave / per, a.T - 1);           // waves past the last token repeat it
+    Choice<P> c(a, t, lane, scratch, beside);
+    int larger[P];
+    c.count_larger(wave % per, per, larger);
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (wave / per < a.T && i * 64 + lane < a.E) atomicAdd(&counts[t * a.E + i * 64 + lane], larger[i]);
+    __syncthreads();
+    if (wave % per == 0 && wave / per < a.T) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) larger[i] = counts[t * a.E + min(i * 64 + lane, a.E - 1)];
+      c.finish(c.order(larger), ids[t], chosen[t], write);
+    }
+    return;
+  }
+  // many experts' keys leave no registers for the others' loads
+  constexpr bool kBeside = P <= 4;
+  bool first = kBeside;
+  for (int t = wave; t < a.T; t += kMlWaves, first = false) {
+    Choice<P> c(a, t, lane, scratch, [&] {
+      if (first) beside();
+    });
+    if constexpr (P <= 2) {
+      int larger[P];
+      c.count_larger(0, 1, larger);
+      c.finish(c.order(larger), ids[t], chosen[t], write);
+    } else {
+      c.finish(c.order(nullptr), ids[t], chosen[t], write);
+    }
+  }
+  if (!kBeside || wave >= a.T) beside();
 }
 
 // ------------------------------------------------------------------ plan
@@ -256,16 +436,15 @@ struct MlTables {
   }
 };
 
-// The active experts, ascending, from plan->ids and plan->chosen. Every thread.
-__device__ __forceinline__ void make_plan(const MlArgs& a, const MlTables& tb) {
-  const int tid = threadIdx.x, lane = tid & 63;
-  for (int e = tid; e < a.E; e += kMlThreads) tb.tokens[e] = 0;
-  for (int i = tid; i < a.most * 16; i += kMlThreads) tb.weight[i] = 0.f;
-  __syncthreads();
-  static_assert(kMlThreads == kMlTokens * kMlMaxK, "a thread per place");
-  const int t = tid / kMlMaxK, j = tid % kMlMaxK;
-  int id = -1;
-  if (t < a.T && j < a.top_k) id = tb.plan->ids[t][j];
+// The active experts, ascending. Thread t * kMlMaxK + j brings token t's j-th choice (id
+// -1: none) and its weight; the tables were cleared in front of a barrier.
+static_assert(kMlThreads == kMlTokens * kMlMaxK, "a thread per choice");
+__device__ __forceinline__ void clear_plan(const MlArgs& a, const MlTables& tb) {
+  for (int e = threadIdx.x; e < a.E; e += kMlThreads) tb.tokens[e] = 0;
+  for (int i = threadIdx.x; i < a.most * 16; i += kMlThreads) tb.weight[i] = 0.f;
+}
+__device__ __forceinline__ void make_plan(const MlArgs& a, const MlTables& tb, int id, float weight) {
+  const int tid = threadIdx.x, lane = tid & 63, t = tid / kMlMaxK, j = tid % kMlMaxK;
   if (id >= 0) atomicOr(&tb.tokens[id], 1u << t);
   __syncthreads();
   if (tid < 64) {
@@ -287,7 +466,7 @@ __device__ __forceinline__ void make_plan(const MlArgs& a, const MlTables& tb) {
   if (id >= 0) {
     const int at = tb.tokens[id];
     tb.place[at * 16 + t] = static_cast<uint8_t>(j);
-    tb.weight[at * 16 + t] = tb.plan->chosen[t][j];
+    tb.weight[at * 16 + t] = weight;
   }
   __syncthreads();
 }
@@ -310,31 +489,47 @@ struct MlWeights {
   uint32_t s[MlUnit<GS>::G];
 };
 
-// Unit u of a block whose packed words and scales start at w and s (already at the
-// lane's place); groups past the last re-read it and are not used.
+// One expert's packed words and scales, as buffers, and whether there is one: loads of an
+// absent one lie past the buffers and return zeros without reading memory, so that
+// every load is issued and the waits stay exact.
+struct MlMatrix {
+  __amdgpu_buffer_rsrc_t w, s;
+  bool there;
+};
+// words, scales: 32-bit words and fp16 scales of one expert's matrix, below 4 GB.
+__device__ __forceinline__ MlMatrix matrix_at(const uint32_t* w, const uint16_t* s, uint32_t words, uint32_t scales,
+                                              int expert, bool there) {
+  return {make_rsrc(w + static_cast<size_t>(expert) * words, words * 4u),
+          make_rsrc(s + static_cast<size_t>(expert) * scales, scales * 2u), there};
+}
+
+// Unit u of a column block whose first tile is `tile` (block * groups); groups past the
+// last are others' and not used.
 template <int GS>
-__device__ __forceinline__ void load_unit(MlWeights<GS>& r, gptr<const uint32_t> w, gptr<const uint32_t> s, int u,
-                                          int groups) {
+__device__ __forceinline__ void load_unit(MlWeights<GS>& r, const MlMatrix& m, int tile, int u, int lane) {
   using U = MlUnit<GS>;
+  constexpr int kOnce = 2;  // the instruction's nt bit
+  const uint32_t far = 0xFFFFFE00u;
+  const uint32_t wl = m.there ? lane * U::WPL * 4 : far, sl = m.there ? (lane & 14) * 2 : far;
 #pragma unroll
   for (int g = 0; g < U::G; ++g) {
-    const int grp = min(u * U::G + g, groups - 1);
-    const gptr<const uint32_t> p = w + static_cast<size_t>(grp) * 64 * U::WPL;
+    const int at = tile + u * U::G + g;
+    const int wat = at * (256 * U::WPL);
     if constexpr (U::WPL >= 4) {
 #pragma unroll
       for (int q = 0; q < U::WPL / 4; ++q) {
-        const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<gptr<const u32x4>>(p) + q);
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(m.w, wl + 16 * q, wat, kOnce);
 #pragma unroll
         for (int i = 0; i < 4; ++i) r.w[g * U::WPL + 4 * q + i] = v[i];
       }
     } else if constexpr (U::WPL == 2) {
-      const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<gptr<const u32x2>>(p));
+      const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(m.w, wl, wat, kOnce);
       r.w[g * 2] = v[0];
       r.w[g * 2 + 1] = v[1];
     } else {
-      r.w[g] = __builtin_nontemporal_load(p);
+      r.w[g] = __builtin_amdgcn_raw_buffer_load_b32(m.w, wl, wat, kOnce);
     }
-    r.s[g] = s[static_cast<size_t>(grp) * 8];
+    r.s[g] = __builtin_amdgcn_raw_buffer_load_b32(m.s, sl, at * 32, 0);
   }
 }
 
@@ -363,10 +558,12 @@ __device__ __forceinline__ float scale_of(uint32_t pair, int lane) {
   return fp16_bits_to_f32(static_cast<uint16_t>(pair >> (16 * (lane & 1))));
 }
 
-// LDS in front of gate_up_kernel's plan: the waves' sums, twice, and before them
-// the choice's scratch, E keys a wave.
-__host__ __device__ constexpr size_t gate_up_scratch(int E) {
-  const size_t sums = 2 * kMlWaves * 2 * 256 * 4, scratch = (static_cast<size_t>(kMlWaves) * E * 8 + 15) / 16 * 16;
+// Bytes of LDS in front of gate_up_kernel's plan: the choice's scratch, E keys a wave and
+// E counts a token; then the waves' sums of a task, twice.
+__host__ __device__ constexpr size_t gate_up_front(int E) {
+  const size_t keys = static_cast<size_t>(kMlWaves) * ((E + 3) / 4 * 4) * 8;
+  const size_t scratch = (keys + (E <= 256 ? 4 * static_cast<size_t>(E) * 4 : 0) + 15) / 16 * 16;
+  const size_t sums = 2 * kMlWaves * 2 * 1024;
   return sums > scratch ? sums : scratch;
 }
 
@@ -377,91 +574,92 @@ __global__ __launch_bounds__(kMlThreads) void gate_up_kernel(const MlArgs a) {
   using U = MlUnit<GS>;
   extern __shared__ __attribute__((aligned(16))) unsigned char ml_lds[];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-  const int c16 = lane & 15;
-  float* const red = reinterpret_cast<float*>(ml_lds);  // [2][waves][2][4][64]
-  constexpr int kRedFloats = kMlWaves * 2 * 256;
-  // the scratch of the choice lies where the sums meet later
-  const MlTables tb(ml_lds + gate_up_scratch(a.E), a.most);
-  // this wave's units of K
-  const int groups = a.H / GS, units = (groups + U::G - 1) / U::G;
-  const int u0 = units * wave / kMlWaves, n = units * (wave + 1) / kMlWaves - u0;
-
-  // The tokens' activations do not need the choice.
+  const int c16 = lane & 15, lg = lane >> 4;
+  float* const red = reinterpret_cast<float*>(ml_lds);
+  const MlTables tb(ml_lds + gate_up_front(a.E), a.most);
+  const bf16x8 bias = bias_operand();
+  // this wave's units of K, and its tokens' activations of them
+  const int up_groups = a.H / GS, up_units = (up_groups + U::G - 1) / U::G;
+  const int u0 = up_units * wave / kMlWaves, n = up_units * (wave + 1) / kMlWaves - u0;
   constexpr int kHeld = KU > 0 ? KU : 1;
   MlRows<GS> x[kHeld];
   // rows past the last token repeat it; no expert's list holds them
   const gptr<const uint16_t> row = to_global(a.x) + static_cast<size_t>(min(c16, a.T - 1)) * a.H;
-  if constexpr (KU > 0) {
+  auto load_x = [&] {
+    if constexpr (KU > 0) {
 #pragma unroll
-    for (int k = 0; k < KU; ++k) load_rows<GS>(x[k], row, min(u0 + k, units - 1), groups);
-  }
-
-  uint64_t* const scratch = reinterpret_cast<uint64_t*>(ml_lds) + static_cast<size_t>(wave) * a.E;
-  for (int t = wave; t < a.T; t += kMlWaves) {
-    short* const ids = tb.plan->ids[t];
-    float* const chosen = tb.plan->chosen[t];
-    if (a.E <= 64)
-      choose<1>(a, t, scratch, lane, ids, chosen);
-    else if (a.E <= 128)
-      choose<2>(a, t, scratch, lane, ids, chosen);
-    else if (a.E <= 256)
-      choose<4>(a, t, scratch, lane, ids, chosen);
-    else if (a.E <= 512)
-      choose<8>(a, t, scratch, lane, ids, chosen);
-    else
-      choose<16>(a, t, scratch, lane, ids, chosen);
-    if (blockIdx.x == 0 && lane < a.top_k) {
-      to_global(a.ids)[t * a.top_k + lane] = ids[lane];
-      to_global(a.weights)[t * a.top_k + lane] = chosen[lane];
+      for (int k = 0; k < KU; ++k) load_rows<GS>(x[k], row, min(u0 + k, up_units - 1), up_groups);
     }
+  };
+
+  clear_plan(a, tb);
+  {
+    uint64_t* const scratch = reinterpret_cast<uint64_t*>(ml_lds);
+    int* const counts = reinterpret_cast<int*>(scratch + static_cast<size_t>(kMlWaves) * ((a.E + 3) / 4 * 4));
+    if (a.T <= 4 && a.E <= 256) {
+      for (int i = tid; i < a.T * a.E; i += kMlThreads) counts[i] = 0;
+      __syncthreads();
+    }
+    const bool write = blockIdx.x == 0;
+    if (a.E <= 64)
+      choose_all<1>(a, scratch, counts, tb.plan->ids, tb.plan->chosen, write, load_x);
+    else if (a.E <= 128)
+      choose_all<2>(a, scratch, counts, tb.plan->ids, tb.plan->chosen, write, load_x);
+    else if (a.E <= 256)
+      choose_all<4>(a, scratch, counts, tb.plan->ids, tb.plan->chosen, write, load_x);
+    else if (a.E <= 512)
+      choose_all<8>(a, scratch, counts, tb.plan->ids, tb.plan->chosen, write, load_x);
+    else
+      choose_all<16>(a, scratch, counts, tb.plan->ids, tb.plan->chosen, write, load_x);
   }
   __syncthreads();
-  make_plan(a, tb);
+  {
+    const int t = tid / kMlMaxK, j = tid % kMlMaxK;
+    const bool there = t < a.T && j < a.top_k;
+    make_plan(a, tb, there ? tb.plan->ids[t][j] : -1, there ? tb.plan->chosen[t][j] : 0.f);
+  }
 
-  const int ct = a.I / 16;  // column blocks of a half
-  const int tasks = tb.plan->active * ct;
-  const size_t words = static_cast<size_t>(2 * ct) * groups * 64 * U::WPL;  // of one expert
-  const size_t scales = static_cast<size_t>(2 * ct) * groups * 16;
-  // the lane's places in the gate and the up block of a task
+  // A task is 16 columns of the gate half and of the up half of an expert.
+  const int ct = a.I / 16;
+  const int tasks = tb.plan->active * ct, stride = gridDim.x;
+  // of one expert
+  const uint32_t up_words = static_cast<uint32_t>(2 * ct) * up_groups * 64 * U::WPL;
+  const uint32_t up_scales = static_cast<uint32_t>(2 * ct) * up_groups * 16;
   struct Where {
-    gptr<const uint32_t> w[2], s[2];
+    MlMatrix m;
+    int tile;  // the gate block's first
   };
+  const int up_tiles = ct * up_groups;  // from a gate block's to its up block's
   auto find = [&](int task) {
-    const int at = task / ct, c = task - at * ct, e = tb.expert[at];
-    Where p;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const size_t b = static_cast<size_t>(c + q * ct) * groups;
-      p.w[q] = to_global(a.gate_up) + e * words + b * 64 * U::WPL + lane * U::WPL;
-      p.s[q] = reinterpret_cast<gptr<const uint32_t>>(to_global(a.gate_up_scales) + e * scales + b * 16 + (c16 & ~1));
-    }
-    return p;
+    const bool there = task < tasks;
+    const int at = there ? task / ct : 0, c = there ? task - at * ct : 0;
+    return Where{matrix_at(a.gate_up, a.gate_up_scales, up_words, up_scales, there ? uniform(tb.expert[at]) : 0, there),
+                 uniform(c * up_groups)};
   };
   constexpr int kAhead = KU > 0 ? KU : 2;
   MlWeights<GS> st[kAhead][2];
   MlRows<GS> xs[KU > 0 ? 1 : kAhead];
-  int task = blockIdx.x;
+  auto load = [&](int k, int slot, const Where& p) {
+    MlMatrix m = p.m;
+    m.there = m.there && k < n;
+    const int u = min(u0 + k, up_units - 1);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) load_unit<GS>(st[slot][q], m, p.tile + q * up_tiles, u, lane);
+    if constexpr (KU == 0) load_rows<GS>(xs[slot], row, u, up_groups);
+  };
+  constexpr int kTaskFloats = kMlWaves * 2 * 256;  // red: [2][waves][2][4][64]
+  int turn = 0, task = blockIdx.x;
   if (task >= tasks) return;
   Where here = find(task);
-  auto load = [&](int k, int slot, const Where& p) {
-    const int u = min(u0 + min(k, max(n, 1) - 1), units - 1);  // past the wave's last: not used
-#pragma unroll
-    for (int q = 0; q < 2; ++q) load_unit<GS>(st[slot][q], p.w[q], p.s[q], u, groups);
-    if constexpr (KU == 0) load_rows<GS>(xs[slot], row, u, groups);
-  };
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) load(k, k, here);
-
-  const bf16x8 bias = bias_operand();
-  int turn = 0;
-  for (; task < tasks; task += gridDim.x) {
-    const int next = task + static_cast<int>(gridDim.x);
-    const Where there = find(min(next, tasks - 1));
+  for (; task < tasks; task += stride) {
+    const Where there = find(task + stride);
     f32x4 y[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     auto unit = [&](const MlRows<GS>& xr, const MlWeights<GS> (&wt)[2], int u) {
 #pragma unroll
       for (int g = 0; g < U::G; ++g) {
-        if (U::G > 1 && u * U::G + g >= groups) break;  // uniform: K ends inside the unit
+        if (U::G > 1 && u * U::G + g >= up_groups) break;  // uniform: K ends inside the unit
         f32x4 accb = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < U::WPL; ++w) accb = mfma16(act_frag(xr.d[g * U::WPL + w]), bias, accb);
@@ -488,17 +686,16 @@ __global__ __launch_bounds__(kMlThreads) void gate_up_kernel(const MlArgs a) {
 #pragma unroll
         for (int p = 0; p < kAhead; ++p) {
           if (k + p < n) unit(xs[p], st[p], u0 + k + p);
-          // the next unit of this task, or past its last one those of the next
-          if (k + p + kAhead < n)
-            load(k + p + kAhead, p, here);
+          if (k + p + kAhead < n) load(k + p + kAhead, p, here);
         }
       }
 #pragma unroll
       for (int p = 0; p < kAhead; ++p) load(p, p, there);
     }
 
-    // the waves' sums, in wave order
-    float* const mine = red + turn * kRedFloats;
+    // the waves' sums, in wave order; consecutive tasks use the two halves in turn, so
+    // one barrier a task is enough
+    float* const mine = red + turn * kTaskFloats;
 #pragma unroll
     for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -506,7 +703,7 @@ __global__ __launch_bounds__(kMlThreads) void gate_up_kernel(const MlArgs a) {
     lds_barrier();
     if (tid < 256) {
       const int at = task / ct, c = task - at * ct;
-      const int t = 4 * (lane >> 4) + (tid >> 6);
+      const int t = 4 * lg + (tid >> 6);
       if (tb.mask[at] >> t & 1) {
         float gate = 0.f, up = 0.f;
 #pragma unroll
@@ -523,181 +720,225 @@ __global__ __launch_bounds__(kMlThreads) void gate_up_kernel(const MlArgs a) {
   }
 }
 
-// AHEAD: units a wave has on the way.
-template <int GS, int AHEAD>
-__global__ __launch_bounds__(kMlThreads) void down_kernel(const MlArgs a) {
+// NB: column blocks of a workgroup, which share the loads of its inner rows; AHEAD: units
+// of them a wave has on the way. INNER: the inner rows fit LDS (inner_bytes), and the long
+// sum the units on the way: nothing is split.
+template <int GS, int NB, int AHEAD, bool INNER>
+__global__ __launch_bounds__(kMlThreads) void down_kernel(const MlArgs a, int most_splits, int inner_bytes) {
   using U = MlUnit<GS>;
   extern __shared__ __attribute__((aligned(16))) unsigned char ml_lds[];
   __shared__ int last_flag;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int c16 = lane & 15, lg = lane >> 4;
-  float* const red = reinterpret_cast<float*>(ml_lds);  // [2][waves][4][64]
-  constexpr int kRedFloats = kMlWaves * 256;
-  const MlTables tb(ml_lds + 2 * kRedFloats * 4, a.most);
+  float* const red = reinterpret_cast<float*>(ml_lds);  // [waves][NB][4][64]
+  unsigned char* const inner = ml_lds + kMlWaves * NB * 1024;  // INNER: [T][top_k][I]
+  const MlTables tb(ml_lds + kMlWaves * NB * 1024 + (INNER ? inner_bytes : 0), a.most);
+  const bf16x8 bias = bias_operand();
+  const int groups = a.I / GS, units = (groups + U::G - 1) / U::G;  // of one expert
+  const int blocks = a.H / 16;
+  const int column = static_cast<int>(blockIdx.x) / most_splits, split = static_cast<int>(blockIdx.x) % most_splits;
+  const int b0 = column * NB;  // first column block
+  int id = -1;
+  float chosen = 0.f;
   {
     const int t = tid / kMlMaxK, j = tid % kMlMaxK;
     if (t < a.T && j < a.top_k) {
-      tb.plan->ids[t][j] = static_cast<short>(to_global(a.ids)[t * a.top_k + j]);
-      tb.plan->chosen[t][j] = to_global(a.weights)[t * a.top_k + j];
+      id = to_global(a.ids)[t * a.top_k + j];
+      chosen = to_global(a.weights)[t * a.top_k + j];
     }
   }
+  const uint32_t h_bytes = static_cast<uint32_t>(a.T * a.top_k) * a.I * 2;
+  const __amdgpu_buffer_rsrc_t rh = make_rsrc(a.h, h_bytes);
+  constexpr int kPieces = INNER ? kMlInnerBytes / (16 * kMlThreads) : 1;
+  u32x4 held[kPieces];  // the inner rows on their way to LDS
+  if constexpr (INNER) {
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p)
+      held[p] = __builtin_amdgcn_raw_buffer_load_b128(rh, (p * kMlThreads + tid) * 16, 0, 0);
+  }
+  // Value i of the tile: block i / 256, row 4 (lane / 16) + i / 64 % 4 and column lane %
+  // 16 of it, lane = i % 64. Whether there is such a value, and what is added to it.
+  auto value_at = [&](int i, int& t, int& col) {
+    t = 4 * ((i & 63) >> 4) + (i >> 6 & 3);
+    col = (b0 + (i >> 8)) * 16 + (i & 15);
+    return t < a.T && col < a.H;
+  };
+  constexpr int kValues = NB * 256 / kMlThreads;  // a thread's
+  static_assert(kValues * kMlThreads == NB * 256, "whole threads");
+  uint16_t base[kValues];
+#pragma unroll
+  for (int j = 0; j < kValues; ++j) {
+    int t, col;
+    const bool there = value_at(tid + j * kMlThreads, t, col);
+    base[j] = there && a.base ? to_global(a.base)[static_cast<size_t>(t) * a.H + col] : 0;
+  }
+  clear_plan(a, tb);
   __syncthreads();
-  make_plan(a, tb);
+  make_plan(a, tb, id, chosen);
 
-  const int groups = a.I / GS, units = (groups + U::G - 1) / U::G;  // of one expert
-  const int blocks = a.H / 16;
-  const int per = tb.plan->active * units;  // units of a column block
-  const long long total = static_cast<long long>(per) * blocks;
-  // the finished values of a block's rows
-  auto write = [&](int b, int t, int col, float v) {
-    const size_t at = static_cast<size_t>(t) * a.H + b * 16 + col;
-    if (a.base) v += bf16_bits_to_f32(to_global(a.base)[at]);
-    to_global(a.out)[at] = f32_to_bf16_bits(v);
-  };
-  if (total == 0) {  // no live token
-    for (int i = blockIdx.x * kMlThreads + tid; i < a.T * a.H; i += gridDim.x * kMlThreads)
-      write(i % a.H / 16, i / a.H, i % 16, 0.f);
-    return;
-  }
-  // every workgroup that takes part holds a unit, so it counts itself in
-  const int NW = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
-  if (static_cast<int>(blockIdx.x) >= NW) return;
-  auto first_of = [&](int w) { return total * w / NW; };
-  // the workgroup that holds a unit
-  auto owner_of = [&](long long u) { return static_cast<int>(((u + 1) * NW - 1) / total); };
-  const long long begin = first_of(blockIdx.x), end = first_of(blockIdx.x + 1);
-  const size_t words = static_cast<size_t>(blocks) * groups * 64 * U::WPL;  // of one expert
-  const size_t scales = static_cast<size_t>(blocks) * groups * 16;
-
-  // The workgroup's units, block by block: a step is a unit for each of its waves,
-  // and a block's last step may leave some without one. Loads run AHEAD steps
-  // before the arithmetic, over the blocks' ends; the two places move alike.
-  struct Walk {
-    int b;                 // block
-    long long pos, stop;   // first unit of the step; end of this block's units here
-  };
-  auto start = [&](Walk& k) {
-    k.b = static_cast<int>(begin / per);
-    k.pos = begin;
-    k.stop = min(end, static_cast<long long>(k.b + 1) * per);
-  };
-  auto advance = [&](Walk& k) {
-    k.pos += kMlWaves;
-    if (k.pos >= k.stop) {
-      k.pos = k.stop;
-      if (k.stop < end) {
-        ++k.b;
-        k.stop = min(end, k.stop + per);
-      }
-    }
-  };
+  const int all = tb.plan->active * units;  // units of the long sum
+  // as many parts as leave every wave a unit
+  const int splits = INNER ? 1 : max(1, min(most_splits, all / kMlWaves));
+  if (split >= splits) return;
+  // of one expert
+  const uint32_t words = static_cast<uint32_t>(blocks) * groups * 64 * U::WPL;
+  const uint32_t scales = static_cast<uint32_t>(blocks) * groups * 16;
   struct Stage {
-    MlWeights<GS> w;
+    MlWeights<GS> w[NB];
     MlRows<GS> h;
     int at, u;  // entry and unit of the expert
   };
-  Stage st[AHEAD];
-  auto load = [&](Stage& s, const Walk& k) {
-    const long long unit = min(k.pos + wave, k.stop - 1);  // past the last: not used
-    const int rest = static_cast<int>(unit - static_cast<long long>(k.b) * per);
-    s.at = rest / units;
-    s.u = rest - s.at * units;
-    const int e = tb.expert[s.at];
-    const size_t off = static_cast<size_t>(k.b) * groups;
-    load_unit<GS>(s.w, to_global(a.down) + e * words + off * 64 * U::WPL + lane * U::WPL,
-                  reinterpret_cast<gptr<const uint32_t>>(to_global(a.down_scales) + e * scales + off * 16 + (c16 & ~1)),
-                  s.u, groups);
-    // rows of other tokens: any row, their results are left out
-    const bool mine = tb.mask[s.at] >> c16 & 1;
-    const size_t slot = mine ? static_cast<size_t>(c16) * a.top_k + tb.place[s.at * 16 + c16] : 0;
-    load_rows<GS>(s.h, to_global(a.h) + slot * a.I, s.u, groups);
-  };
-  Walk now, then;
-  start(now);
-  start(then);
+  Stage ds[AHEAD];
+  // a wave's way through the units of its part: every kMlWaves-th of them
+  const int first = static_cast<int>(static_cast<long long>(all) * split / splits) + wave;
+  const int end = static_cast<int>(static_cast<long long>(all) * (split + 1) / splits);
+  const int n = max(0, (end - first + kMlWaves - 1) / kMlWaves);
+  const int at_step = kMlWaves / units, u_step = kMlWaves - at_step * units;
+  int next_at = first / units, next_u = first - next_at * units, left = n;
+  auto load_weights = [&](Stage& s) {
+    const bool there = left > 0;
+    s.at = there ? next_at : -1;
+    s.u = there ? next_u : 0;
+    const MlMatrix m =
+        matrix_at(a.down, a.down_scales, words, scales, there ? uniform(tb.expert[next_at]) : 0, there);
 #pragma unroll
-  for (int p = 0; p < AHEAD; ++p) {
-    load(st[p], then);
-    advance(then);
+    for (int b = 0; b < NB; ++b) {
+      MlMatrix mb = m;
+      mb.there = there && b0 + b < blocks;
+      load_unit<GS>(s.w[b], mb, min(b0 + b, blocks - 1) * groups, s.u, lane);
+    }
+    next_at += at_step;
+    next_u += u_step;
+    if (next_u >= units) {
+      next_u -= units;
+      ++next_at;
+    }
+    --left;
+    __builtin_amdgcn_sched_barrier(0);  // one unit's buffers in scalar registers at a time
+  };
+  auto load_inner = [&](Stage& s) {
+    // other tokens' rows lie past the buffer and read as zeros, as do groups past
+    // the last (its end is one of them)
+    const bool mine = s.at >= 0 && tb.mask[s.at] >> c16 & 1;
+    const uint32_t slot = mine ? c16 * a.top_k + tb.place[s.at * 16 + c16] : 0;
+#pragma unroll
+    for (int g = 0; g < U::G; ++g) {
+      const int grp = s.u * U::G + g;
+      const uint32_t at = mine && grp < groups ? (slot * a.I + grp * GS + lg * U::WPL * 8) * 2 : 0xFFFFFE00u;
+#pragma unroll
+      for (int w = 0; w < U::WPL; ++w)
+        s.h.d[g * U::WPL + w] = __builtin_amdgcn_raw_buffer_load_b128(rh, at, 16 * w, 0);
+    }
+  };
+  // the same from LDS, where any row stands for those of other tokens
+  auto read_inner = [&](Stage& s) {
+    const bool mine = tb.mask[s.at] >> c16 & 1;
+    const uint32_t slot = mine ? c16 * a.top_k + tb.place[s.at * 16 + c16] : 0;
+#pragma unroll
+    for (int g = 0; g < U::G; ++g) {
+      const int grp = min(s.u * U::G + g, groups - 1);
+#pragma unroll
+      for (int w = 0; w < U::WPL; ++w)
+        s.h.d[g * U::WPL + w] =
+            *reinterpret_cast<const u32x4*>(inner + (slot * a.I + grp * GS + (lg * U::WPL + w) * 8) * 2);
+    }
+  };
+#pragma unroll
+  for (int p = 0; p < AHEAD; ++p) load_weights(ds[p]);
+  if constexpr (INNER) {
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p)
+      if ((p * kMlThreads + tid) * 16 < static_cast<int>(h_bytes))
+        *reinterpret_cast<u32x4*>(inner + (p * kMlThreads + tid) * 16) = held[p];
+    lds_barrier();
   }
-
-  const bf16x8 bias = bias_operand();
-  f32x4 y = {0.f, 0.f, 0.f, 0.f};
-  auto unit = [&](const Stage& s) {
+  if constexpr (!INNER) {
+#pragma unroll
+    for (int p = 0; p < AHEAD; ++p) load_inner(ds[p]);
+  }
+  f32x4 y[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) y[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto unit = [&](Stage& s) {
+    if constexpr (INNER) read_inner(s);
     const f32x4 wt = *reinterpret_cast<const f32x4*>(tb.weight + s.at * 16 + 4 * lg);
     const int live = static_cast<uint16_t>(tb.mask[s.at]) >> (4 * lg);
 #pragma unroll
     for (int g = 0; g < U::G; ++g) {
       if (U::G > 1 && s.u * U::G + g >= groups) break;  // uniform: K ends inside the unit
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      f32x4 accb = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < U::WPL; ++w) acc = mfma16(act_frag(s.h.d[g * U::WPL + w]), bias, acc);
+      for (int w = 0; w < U::WPL; ++w) accb = mfma16(act_frag(s.h.d[g * U::WPL + w]), bias, accb);
 #pragma unroll
-      for (int w = 0; w < U::WPL; ++w)
-        acc = mfma16(act_frag(s.h.d[g * U::WPL + w]), dequant_biased(s.w.w[g * U::WPL + w]), acc);
-      const float sc = scale_of(s.w.s[g], lane);
-      // a row that is not the expert's takes nothing from it, whatever its values
+      for (int b = 0; b < NB; ++b) {
+        f32x4 acc = accb;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) y[r] = live >> r & 1 ? __builtin_fmaf(sc * wt[r], acc[r], y[r]) : y[r];
+        for (int w = 0; w < U::WPL; ++w)
+          acc = mfma16(act_frag(s.h.d[g * U::WPL + w]), dequant_biased(s.w[b].w[g * U::WPL + w]), acc);
+        const float sc = scale_of(s.w[b].s[g], lane);
+        // a row that is not the expert's takes nothing from it, whatever its values
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          y[b][r] = live >> r & 1 ? __builtin_fmaf(sc * wt[r], acc[r], y[b][r]) : y[b][r];
+      }
     }
   };
-  int turn = 0, side = 0;
-  // the end of the units [seg, stop) of block b
-  auto finish = [&](int b, long long stop) {
-    float* const mine = red + turn * kRedFloats;
-    turn ^= 1;
+  if constexpr (INNER) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) mine[(wave * 4 + r) * 64 + lane] = y[r];
-    y = f32x4{0.f, 0.f, 0.f, 0.f};
-    lds_barrier();
-    const int t = 4 * lg + (tid >> 6);  // of threads 0 .. 255
+    for (int p = 0; p < AHEAD; ++p)
+      if (p < n) unit(ds[p]);
+  } else {
+    for (int k = 0; k < n; k += AHEAD) {
+#pragma unroll
+      for (int p = 0; p < AHEAD; ++p) {
+        if (k + p < n) unit(ds[p]);
+        load_weights(ds[p]);
+        load_inner(ds[p]);
+      }
+    }
+  }
+
+  // the waves' sums, in wave order
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) red[((wave * NB + b) * 4 + r) * 64 + lane] = y[b][r];
+  lds_barrier();
+  auto write = [&](int t, int col, float v, uint16_t base_bits) {
+    if (a.base) v += bf16_bits_to_f32(base_bits);
+    to_global(a.out)[static_cast<size_t>(t) * a.H + col] = f32_to_bf16_bits(v);
+  };
+  float* const part = a.parts + static_cast<size_t>(column) * most_splits * NB * 256;
+#pragma unroll
+  for (int j = 0; j < kValues; ++j) {
+    const int i = tid + j * kMlThreads;
+    int t, col;
+    if (!value_at(i, t, col)) continue;
     float v = 0.f;
-    if (tid < 256) {
 #pragma unroll
-      for (int w = 0; w < kMlWaves; ++w) v += mine[(w * 4 + (tid >> 6)) * 64 + lane];
-    }
-    const long long b0 = static_cast<long long>(b) * per;
-    if (begin <= b0 && stop == b0 + per) {
-      if (tid < 256 && t < a.T) write(b, t, c16, v);
-    } else {
-      // The block lies with several workgroups: the last to count itself in adds
-      // the parts in the order of the workgroups. A workgroup's part of the block
-      // it starts in is its first, of a later one its second.
-      const int w0 = owner_of(b0), w1 = owner_of(b0 + per - 1);
-      if (tid < 256)
-        __hip_atomic_store(a.parts + (static_cast<size_t>(blockIdx.x) * 2 + side) * kMlPartFloats + tid, v,
-                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      wait_vmem_all();
-      __syncthreads();
-      if (tid == 0)
-        last_flag = __hip_atomic_fetch_add(a.counters + b, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == w1 - w0;
-      __syncthreads();
-      if (last_flag && tid < 256 && t < a.T) {
-        float s = 0.f;
-        for (int w = w0; w <= w1; ++w) {
-          const int its = first_of(w) >= b0 ? 0 : 1;
-          s += __hip_atomic_load(a.parts + (static_cast<size_t>(w) * 2 + its) * kMlPartFloats + tid, __ATOMIC_RELAXED,
-                                 __HIP_MEMORY_SCOPE_AGENT);
-        }
-        write(b, t, c16, s);
-      }
-    }
-    side = 1;
-  };
-  for (bool done = false; !done;) {
+    for (int w = 0; w < kMlWaves; ++w) v += red[w * NB * 256 + i];
+    if (splits == 1)
+      write(t, col, v, base[j]);
+    else
+      __hip_atomic_store(part + split * NB * 256 + i, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (splits == 1) return;
+  // The last of the splits to count itself in adds their parts, in their order.
+  wait_vmem_all();
+  __syncthreads();
+  if (tid == 0)
+    last_flag = __hip_atomic_fetch_add(a.counters + column, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == splits - 1;
+  __syncthreads();
+  if (!last_flag) return;
 #pragma unroll
-    for (int p = 0; p < AHEAD; ++p) {
-      if (done) continue;
-      if (now.pos + wave < now.stop) unit(st[p]);
-      load(st[p], then);
-      advance(then);
-      const Walk was = now;
-      advance(now);
-      if (was.pos + kMlWaves >= was.stop) {
-        finish(was.b, was.stop);
-        done = was.stop >= end;
-      }
-    }
+  for (int j = 0; j < kValues; ++j) {
+    const int i = tid + j * kMlThreads;
+    int t, col;
+    if (!value_at(i, t, col)) continue;
+    float v = 0.f;
+    for (int s = 0; s < splits; ++s)
+      v += __hip_atomic_load(part + s * NB * 256 + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    write(t, col, v, base[j]);
   }
 }
 
@@ -710,9 +951,27 @@ hipError_t with_lds(F* kernel, size_t lds) {
                              static_cast<int>(lds));
 }
 
+template <bool HALF>
+hipError_t launch_router(const MlArgs& a, hipStream_t stream) {
+  // as few rounds as 1024 threads allow, and no more threads than they need
+  const int pieces = a.H / 8, rounds = (pieces + kMlRouterThreads - 1) / kMlRouterThreads;
+  const int threads = ((pieces + rounds - 1) / rounds + 63) / 64 * 64;
+  if (a.T == 1)
+    router_kernel<HALF, 1><<<dim3(a.E), dim3(threads), 0, stream>>>(a);
+  else if (a.T == 2)
+    router_kernel<HALF, 2><<<dim3(a.E), dim3(threads), 0, stream>>>(a);
+  else if (a.T <= 4)
+    router_kernel<HALF, 4><<<dim3(a.E), dim3(threads), 0, stream>>>(a);
+  else if (a.T <= 8)
+    router_kernel<HALF, 8><<<dim3(a.E), dim3(threads), 0, stream>>>(a);
+  else
+    router_kernel<HALF, 16><<<dim3(a.E), dim3(threads), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
 template <int GS, int KU>
 hipError_t launch_gate_up(const MlArgs& a, hipStream_t stream) {
-  const size_t lds = gate_up_scratch(a.E) + ml_plan_bytes(a.most, a.E);
+  const size_t lds = gate_up_front(a.E) + ml_plan_bytes(a.most, a.E);
   auto* kernel = &gate_up_kernel<GS, KU>;
   const hipError_t e = with_lds(kernel, lds);
   if (e != hipSuccess) return e;
@@ -722,35 +981,45 @@ hipError_t launch_gate_up(const MlArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <int GS, int NB, int AHEAD, bool INNER>
+hipError_t launch_down(const MlArgs& a, hipStream_t stream) {
+  const int inner = INNER ? a.T * a.top_k * a.I * 2 : 0;
+  const size_t lds = static_cast<size_t>(kMlWaves) * NB * 1024 + inner + ml_plan_bytes(a.most, a.E);
+  auto* kernel = &down_kernel<GS, NB, AHEAD, INNER>;
+  const hipError_t e = with_lds(kernel, lds);
+  if (e != hipSuccess) return e;
+  const int columns = (a.H / 16 + NB - 1) / NB;
+  const int splits = INNER || columns >= kModelCUs ? 1 : kModelCUs / columns;
+  kernel<<<dim3(columns * splits), dim3(kMlThreads), lds, stream>>>(a, splits, inner);
+  return hipGetLastError();
+}
+
 template <int GS>
 hipError_t launch_moe_layer_g(const MlArgs& a, bool half, hipStream_t stream) {
   using U = MlUnit<GS>;
-  if (half)
-    router_kernel<true><<<dim3(a.E), dim3(kMlRouterThreads), 0, stream>>>(a);
-  else
-    router_kernel<false><<<dim3(a.E), dim3(kMlRouterThreads), 0, stream>>>(a);
-  hipError_t e = hipGetLastError();
+  hipError_t e = half ? launch_router<true>(a, stream) : launch_router<false>(a, stream);
   if (e != hipSuccess) return e;
-  const int groups = a.H / GS, units = (groups + U::G - 1) / U::G;
-  const int held = (units + kMlWaves - 1) / kMlWaves * U::F / 4;  // 128s of K per wave
+  constexpr int kPer = U::K / 128;
+  const int held = ((a.H / GS + U::G - 1) / U::G + kMlWaves - 1) / kMlWaves * kPer;  // 128s of K per wave
   if (held <= 2)
-    e = launch_gate_up<GS, 2 * 4 / U::F>(a, stream);
+    e = launch_gate_up<GS, 2 / kPer>(a, stream);
   else if (held <= 4)
-    e = launch_gate_up<GS, 4 * 4 / U::F>(a, stream);
-  else if (held == 5 && U::F == 4)
-    e = launch_gate_up<GS, U::F == 4 ? 5 : 0>(a, stream);
+    e = launch_gate_up<GS, 4 / kPer>(a, stream);
+  else if (held == 5 && kPer == 1)
+    e = launch_gate_up<GS, kPer == 1 ? 5 : 0>(a, stream);
   else if (held <= 6)
-    e = launch_gate_up<GS, 6 * 4 / U::F>(a, stream);
+    e = launch_gate_up<GS, 6 / kPer>(a, stream);
   else
     e = launch_gate_up<GS, 0>(a, stream);
   if (e != hipSuccess) return e;
-  const size_t lds = 2 * kMlWaves * 256 * 4 + ml_plan_bytes(a.most, a.E);
-  constexpr int kAhead = U::F == 4 ? 4 : 2;
-  auto* kernel = &down_kernel<GS, kAhead>;
-  e = with_lds(kernel, lds);
-  if (e != hipSuccess) return e;
-  kernel<<<dim3(kModelCUs), dim3(kMlThreads), lds, stream>>>(a);
-  return hipGetLastError();
+  // The long sum of few active experts is on its way as a whole, and their inner rows
+  // fit LDS; else it is split and streamed.
+  constexpr int kShort = U::F == 4 ? 8 : 4;
+  const int units = (a.I / GS + U::G - 1) / U::G;
+  if (static_cast<long long>(a.most) * units <= kMlWaves * kShort &&
+      static_cast<long long>(a.T) * a.top_k * a.I * 2 <= kMlInnerBytes)
+    return launch_down<GS, 2, kShort, true>(a, stream);
+  return launch_down<GS, 4, U::F == 4 ? 2 : 1, false>(a, stream);
 }
 
 }  // namespace
