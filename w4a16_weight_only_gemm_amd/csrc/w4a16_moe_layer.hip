@@ -183,35 +183,50 @@ __device__ __forceinline__ int take_one(uint32_t (&hi)[P], uint32_t (&lo)[P], in
   return e;
 }
 
+// Two keys of a group, the larger first, with another lane's two.
+__device__ __forceinline__ void merge_two(uint64_t& first, uint64_t& second, uint64_t f, uint64_t s) {
+  const uint64_t low = f < first ? f : first, high = s > second ? s : second;
+  first = f > first ? f : first;
+  second = low > high ? low : high;
+}
+
 // One token's experts by the rule of w4a16_moe_route, in fp64 throughout; a wave does
-// all of it, or several share the comparisons. P: experts per lane, expert i * 64 +
-// lane the i-th.
+// all of it, or the part-th of several a share of the scores and of the comparisons. P: experts per lane, expert i * 64 + lane the i-th.
 template <int P>
 struct Choice {
   const MlArgs& a;
-  int t, lane;
+  int t, lane, part, parts;
   uint64_t* scratch;  // E keys of LDS, the wave's own
   gptr<const double> logits;
   uint64_t key[P];  // of the logits, then of the choice values; 0: cannot be chosen
   double most, sum;
 
   static __device__ __forceinline__ double finite(double v) { return (v > DBL_MAX ? DBL_MAX : v) + 0.0; }  // -0 is 0
-  __device__ __forceinline__ double score(double z) const {
-    return a.sigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - most) / sum;
+  // a score, but for softmax's division by the sum
+  __device__ __forceinline__ double raw_score(double z) const {
+    return a.sigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - most);
   }
 
-  // beside: loads that may come behind the logits'
+  // shared: with several parts, E scores of LDS of the token and then their sums by 64.
+  // beside: loads that may come behind the logits'.
   template <typename F>
-  __device__ __forceinline__ Choice(const MlArgs& args, int token, int lane_, uint64_t* scratch_, F beside)
-      : a(args), t(token), lane(lane_), scratch(scratch_), most(0.0), sum(1.0) {
+  __device__ __forceinline__ Choice(const MlArgs& args, int token, int lane_, int part_, int parts_,
+                                    uint64_t* scratch_, double* shared, F beside)
+      : a(args), t(token), lane(lane_), part(part_), parts(parts_), scratch(scratch_), most(0.0), sum(1.0) {
     logits = to_global(a.logits) + static_cast<size_t>(t) * a.E;
+    const int live = a.live ? to_global(a.live)[t] : 1;
     double z[P];
+    float bias[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) z[i] = logits[min(i * 64 + lane, a.E - 1)];
+    for (int i = 0; i < P; ++i) {
+      const int e = min(i * 64 + lane, a.E - 1);
+      z[i] = logits[e];
+      bias[i] = a.route_bias ? to_global(a.route_bias)[e] : 0.f;
+    }
     __builtin_amdgcn_sched_barrier(0);
     beside();
     __builtin_amdgcn_sched_barrier(0);
-    const bool here = !a.live || a.live[t] != 0;
+    const bool here = live != 0;
     uint64_t m = 0;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -219,68 +234,85 @@ struct Choice {
       key[i] = open ? order_key(finite(z[i])) : 0;
       m = key[i] > m ? key[i] : m;
     }
-    const bool by_value = a.route_bias || a.groups > 1;
     if (!a.sigmoid) {
       m = wave_max_of(m);
       most = m ? value_of(m) : 0.0;
-      // a sum over all experts divides every score: it matters unless experts are
-      // compared by their logits and scores are divided by their own sum
-      if (by_value || !a.renormalize) {
-        sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          sum += key[i] ? exp(value_of(key[i]) - most) : 0.0;
-          __builtin_amdgcn_sched_barrier(0);  // one exponential's registers at a time
-        }
-        sum = wave_sum_of(sum);
-      }
     }
-    if (by_value) {
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const int e = i * 64 + lane;
-        const double bias = a.route_bias && e < a.E ? to_global(a.route_bias)[e] : 0.f;
-        if (key[i]) key[i] = order_key(score(value_of(key[i])) + bias + 0.0);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
+    // Scores over all experts matter unless experts are compared by their logits and
+    // scores are divided by the sum of the chosen.
+    const bool by_value = a.route_bias || a.groups > 1;
+    if (by_value || (!a.sigmoid && !a.renormalize)) score_all(shared, by_value, bias);
     if (a.groups > 1) keep_groups();
   }
 
+  __device__ __forceinline__ void score_all(double* shared, bool by_value, const float (&bias)[P]) {
+    double score[P];
+    double by64[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      score[i] = by64[i] = 0.0;
+      if (parts > 1 && i % parts != part) continue;
+      score[i] = key[i] ? raw_score(value_of(key[i])) : 0.0;
+      if (!a.sigmoid) by64[i] = wave_sum_of(score[i]);
+      __builtin_amdgcn_sched_barrier(0);  // one exponential's registers at a time
+      if (parts > 1) {
+        if (i * 64 + lane < a.E) shared[i * 64 + lane] = score[i];
+        if (lane == 0) shared[a.E + i] = by64[i];
+      }
+    }
+    if (parts > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        if (i % parts == part) continue;
+        score[i] = shared[min(i * 64 + lane, a.E - 1)];
+        by64[i] = shared[a.E + i];
+      }
+    }
+    if (!a.sigmoid) {
+      sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < P; ++i) sum += by64[i];
+    }
+    if (!by_value) return;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (key[i]) key[i] = order_key(score[i] / sum + static_cast<double>(bias[i]) + 0.0);
+  }
+
   __device__ __forceinline__ void keep_groups() {
-    // lane g looks at group g: its largest value, or the sum of its two largest
+    // A group's largest value, or the sum of its two largest, from a run of lanes: 64
+    // over the groups, rounded up to a power of two. Lane g * run holds group g's.
 #pragma unroll
     for (int i = 0; i < P; ++i)
       if (i * 64 + lane < a.E) scratch[i * 64 + lane] = key[i];
     wave_sync();
     const int per = a.E / a.groups;
+    const int shift = a.groups <= 1 ? 6 : __builtin_clz(a.groups - 1) - 26, run = 1 << shift;
+    const int g = lane >> shift;
     uint64_t first = 0, second = 0;
-    if (lane < a.groups)
-      for (int i = 0; i < per; ++i) {
-        const uint64_t k = scratch[lane * per + i];
-        const uint64_t lower = k < first ? k : first;
-        first = k > first ? k : first;
-        second = lower > second ? lower : second;
-      }
+    if (g < a.groups)
+      for (int i = lane & (run - 1); i < per; i += run) merge_two(first, second, scratch[g * per + i], 0);
+    for (int o = 1; o < run; o <<= 1) merge_two(first, second, __shfl_xor(first, o), __shfl_xor(second, o));
     uint64_t value = first;
     if (a.group_top == 2 && second) value = order_key(value_of(first) + value_of(second) + 0.0);
     int rank = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const uint64_t other = lane_of(value, g);
-      rank += other > value || (other == value && g < lane);
+    for (int o = 0; o < a.groups; ++o) {
+      const uint64_t other = lane_of(value, o << shift);
+      rank += other > value || (other == value && o < g);
     }
-    const uint64_t kept = __ballot(lane < a.groups && rank < a.groups_kept);
+    const uint64_t kept = __ballot(g < a.groups && rank < a.groups_kept);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int e = i * 64 + lane;
-      if (e < a.E && !(kept >> (e / per) & 1)) key[i] = 0;
+      if (e < a.E && !(kept >> (e / per << shift) & 1)) key[i] = 0;
     }
     wave_sync();
   }
 
-  // How many of the experts of the part-th of `parts` ranges have a larger high word,
+  // How many of the experts of the part-th of the parts' ranges have a larger high word,
   // for each of the lane's.
-  __device__ __forceinline__ void count_larger(int part, int parts, int (&larger)[P]) const {
+  __device__ __forceinline__ void count_larger(int (&larger)[P]) const {
     uint32_t* const words = reinterpret_cast<uint32_t*>(scratch);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -340,7 +372,7 @@ struct Choice {
 
   // ids and weights of the token; `write`: to the caller's arrays too.
   __device__ __forceinline__ void finish(int id, short* ids, float* weights, bool write) const {
-    double w = id >= 0 ? score(finite(logits[id])) : 0.0;
+    double w = id >= 0 ? raw_score(finite(logits[id])) / sum : 0.0;
     if (a.renormalize) {
       const double s = wave_sum_of(w);
       w = s > 0.0 ? w / s : 0.0;
@@ -356,51 +388,74 @@ struct Choice {
   }
 };
 
-// All tokens' experts, into ids[token][kMlMaxK] and chosen. Every thread. counts: E ints
-// of LDS for every token while a token has several waves. Up to 4 tokens share the waves
-// evenly, so that a token's E^2 comparisons are spread over 8 to 2 of them; with more
-// tokens a wave has tokens of its own, and compares where that is less work than
-// top_k rounds over the wave (128 experts, 8 choices: 0.9 against 1.8 us a token; 256:
-// twice the rounds).
-// beside: loads of every wave that are wanted behind the choice.
+// LDS of a choice: E keys a wave; E + P doubles and E counts for each token whose work
+// several waves share.
+__host__ __device__ constexpr size_t choice_bytes(int E, int shared_tokens) {
+  const size_t keys = static_cast<size_t>(kMlWaves) * ((E + 3) / 4 * 4) * 8;
+  return (keys + shared_tokens * ((static_cast<size_t>(E) + 16) * 8 + static_cast<size_t>(E) * 4) + 15) / 16 * 16;
+}
+
+// The experts of tokens t0 .. t0 + T - 1 (T = 1 or 2), the waves shared evenly, into
+// ids[i][kMlMaxK] and chosen of the i-th. Every thread. Places are counted where that is
+// less work than top_k rounds over the wave (128 experts on 8 waves 0.3 us, a round some
+// 0.2; 256 experts 0.9, a round 0.4). beside: loads of every wave that are wanted behind
+// the choice.
 template <int P, typename F>
-__device__ __forceinline__ void choose_all(const MlArgs& a, uint64_t* scratch, int* counts, short (*ids)[kMlMaxK],
-                                           float (*chosen)[kMlMaxK], bool write, F beside) {
+__device__ __forceinline__ void choose_together(const MlArgs& a, int t0, int T, unsigned char* lds,
+                                                short (*ids)[kMlMaxK], float (*chosen)[kMlMaxK], bool write, F beside) {
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-  scratch += static_cast<size_t>(wave) * ((a.E + 3) / 4 * 4);
-  if (a.T <= 4 && P <= 4) {
-    const int per = a.T == 1 ? 8 : a.T == 2 ? 4 : 2;  // waves a token
-    const int t = min(wave / per, a.T - 1);           // waves past the last token repeat it
-    Choice<P> c(a, t, lane, scratch, beside);
-    int larger[P];
-    c.count_larger(wave % per, per, larger);
+  const int keys = (a.E + 3) / 4 * 4;
+  double* const shared = reinterpret_cast<double*>(lds) + kMlWaves * keys;
+  int* const counts = reinterpret_cast<int*>(shared + T * (a.E + 16));
+  for (int i = tid; i < T * a.E; i += kMlThreads) counts[i] = 0;
+  __syncthreads();
+  const int parts = kMlWaves / T, i0 = wave / parts;
+  Choice<P> c(a, t0 + i0, lane, wave % parts, parts, reinterpret_cast<uint64_t*>(lds) + wave * keys,
+              shared + i0 * (a.E + 16), beside);
+  int larger[P];
+  const bool count = P * P <= 4 * parts;
+  if (count) {
+    c.count_larger(larger);
 #pragma unroll
     for (int i = 0; i < P; ++i)
-      if (wave / per < a.T && i * 64 + lane < a.E) atomicAdd(&counts[t * a.E + i * 64 + lane], larger[i]);
+      if (i * 64 + lane < a.E) atomicAdd(&counts[i0 * a.E + i * 64 + lane], larger[i]);
     __syncthreads();
-    if (wave % per == 0 && wave / per < a.T) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) larger[i] = counts[t * a.E + min(i * 64 + lane, a.E - 1)];
-      c.finish(c.order(larger), ids[t], chosen[t], write);
-    }
-    return;
+    for (int i = 0; i < P; ++i) larger[i] = counts[i0 * a.E + min(i * 64 + lane, a.E - 1)];
   }
-  // many experts' keys leave no registers for the others' loads
-  constexpr bool kBeside = P <= 4;
-  bool first = kBeside;
+  if (wave % parts == 0) c.finish(c.order(count ? larger : nullptr), ids[i0], chosen[i0], write);
+}
+
+// All tokens' experts, up to 64 of them, a wave for a token.
+template <typename F>
+__device__ __forceinline__ void choose_each(const MlArgs& a, unsigned char* lds, short (*ids)[kMlMaxK],
+                                            float (*chosen)[kMlMaxK], bool write, F beside) {
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  bool first = true;
   for (int t = wave; t < a.T; t += kMlWaves, first = false) {
-    Choice<P> c(a, t, lane, scratch, [&] {
+    Choice<1> c(a, t, lane, 0, 1, reinterpret_cast<uint64_t*>(lds) + wave * 64, nullptr, [&] {
       if (first) beside();
     });
-    if constexpr (P <= 2) {
-      int larger[P];
-      c.count_larger(0, 1, larger);
-      c.finish(c.order(larger), ids[t], chosen[t], write);
-    } else {
-      c.finish(c.order(nullptr), ids[t], chosen[t], write);
-    }
+    int larger[1];
+    c.count_larger(larger);
+    c.finish(c.order(larger), ids[t], chosen[t], write);
   }
-  if (!kBeside || wave >= a.T) beside();
+  if (wave >= a.T) beside();
+}
+
+// Whether every workgroup of gate_up_kernel makes the choice itself: for one or two
+// tokens, whose work 8 waves share, and for few experts. Otherwise a launch of its own, a
+// workgroup per token, is ahead (us of gate_up_kernel before its first weights, of both
+// launches with one: 4 tokens of 256 experts in groups 12.2 / 7.6, 16 of 128 12.9 / 7.1;
+// 1 of 128 4.5 / 6.7).
+__host__ __device__ constexpr bool choose_inside(int T, int E) { return E <= 64 || (T <= 2 && E <= 256); }
+
+template <int P>
+__global__ __launch_bounds__(kMlThreads) void choose_kernel(const MlArgs a) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char ml_lds[];
+  __shared__ short ids[1][kMlMaxK];
+  __shared__ float chosen[1][kMlMaxK];
+  choose_together<P>(a, blockIdx.x, 1, ml_lds, ids, chosen, true, [] {});
 }
 
 // ------------------------------------------------------------------ plan
@@ -558,13 +613,12 @@ __device__ __forceinline__ float scale_of(uint32_t pair, int lane) {
   return fp16_bits_to_f32(static_cast<uint16_t>(pair >> (16 * (lane & 1))));
 }
 
-// Bytes of LDS in front of gate_up_kernel's plan: the choice's scratch, E keys a wave and
-// E counts a token; then the waves' sums of a task, twice.
-__host__ __device__ constexpr size_t gate_up_front(int E) {
-  const size_t keys = static_cast<size_t>(kMlWaves) * ((E + 3) / 4 * 4) * 8;
-  const size_t scratch = (keys + (E <= 256 ? 4 * static_cast<size_t>(E) * 4 : 0) + 15) / 16 * 16;
+// Bytes of LDS in front of gate_up_kernel's plan: the choice's, then the waves' sums of a
+// task, twice.
+__host__ __device__ constexpr size_t gate_up_front(int T, int E) {
+  const size_t choice = choose_inside(T, E) ? choice_bytes(E < 64 ? 64 : E, 2) : 0;
   const size_t sums = 2 * kMlWaves * 2 * 1024;
-  return sums > scratch ? sums : scratch;
+  return sums > choice ? sums : choice;
 }
 
 // KU: units of K per wave, held in registers (0: any number, read again for every
@@ -576,7 +630,7 @@ __global__ __launch_bounds__(kMlThreads) void gate_up_kernel(const MlArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int c16 = lane & 15, lg = lane >> 4;
   float* const red = reinterpret_cast<float*>(ml_lds);
-  const MlTables tb(ml_lds + gate_up_front(a.E), a.most);
+  const MlTables tb(ml_lds + gate_up_front(a.T, a.E), a.most);
   const bf16x8 bias = bias_operand();
   // this wave's units of K, and its tokens' activations of them
   const int up_groups = a.H / GS, up_units = (up_groups + U::G - 1) / U::G;
@@ -593,31 +647,34 @@ __global__ __launch_bounds__(kMlThreads) void gate_up_kernel(const MlArgs a) {
   };
 
   clear_plan(a, tb);
-  {
-    uint64_t* const scratch = reinterpret_cast<uint64_t*>(ml_lds);
-    int* const counts = reinterpret_cast<int*>(scratch + static_cast<size_t>(kMlWaves) * ((a.E + 3) / 4 * 4));
-    if (a.T <= 4 && a.E <= 256) {
-      for (int i = tid; i < a.T * a.E; i += kMlThreads) counts[i] = 0;
-      __syncthreads();
-    }
+  int id = -1;
+  float weight = 0.f;
+  const int t = tid / kMlMaxK, j = tid % kMlMaxK;
+  const bool place = t < a.T && j < a.top_k;
+  if (choose_inside(a.T, a.E)) {
     const bool write = blockIdx.x == 0;
-    if (a.E <= 64)
-      choose_all<1>(a, scratch, counts, tb.plan->ids, tb.plan->chosen, write, load_x);
+    if (a.T > 2)
+      choose_each(a, ml_lds, tb.plan->ids, tb.plan->chosen, write, load_x);
+    else if (a.E <= 64)
+      choose_together<1>(a, 0, a.T, ml_lds, tb.plan->ids, tb.plan->chosen, write, load_x);
     else if (a.E <= 128)
-      choose_all<2>(a, scratch, counts, tb.plan->ids, tb.plan->chosen, write, load_x);
-    else if (a.E <= 256)
-      choose_all<4>(a, scratch, counts, tb.plan->ids, tb.plan->chosen, write, load_x);
-    else if (a.E <= 512)
-      choose_all<8>(a, scratch, counts, tb.plan->ids, tb.plan->chosen, write, load_x);
+      choose_together<2>(a, 0, a.T, ml_lds, tb.plan->ids, tb.plan->chosen, write, load_x);
     else
-      choose_all<16>(a, scratch, counts, tb.plan->ids, tb.plan->chosen, write, load_x);
+      choose_together<4>(a, 0, a.T, ml_lds, tb.plan->ids, tb.plan->chosen, write, load_x);
+    __syncthreads();
+    if (place) {
+      id = tb.plan->ids[t][j];
+      weight = tb.plan->chosen[t][j];
+    }
+  } else {
+    if (place) {
+      id = to_global(a.ids)[t * a.top_k + j];
+      weight = to_global(a.weights)[t * a.top_k + j];
+    }
+    load_x();
+    __syncthreads();
   }
-  __syncthreads();
-  {
-    const int t = tid / kMlMaxK, j = tid % kMlMaxK;
-    const bool there = t < a.T && j < a.top_k;
-    make_plan(a, tb, there ? tb.plan->ids[t][j] : -1, there ? tb.plan->chosen[t][j] : 0.f);
-  }
+  make_plan(a, tb, id, weight);
 
   // A task is 16 columns of the gate half and of the up half of an expert.
   const int ct = a.I / 16;
@@ -951,6 +1008,23 @@ hipError_t with_lds(F* kernel, size_t lds) {
                              static_cast<int>(lds));
 }
 
+template <int P>
+hipError_t launch_choose_t(const MlArgs& a, hipStream_t stream) {
+  auto* kernel = &choose_kernel<P>;
+  const size_t lds = choice_bytes(a.E, 1);
+  const hipError_t e = with_lds(kernel, lds);
+  if (e != hipSuccess) return e;
+  kernel<<<dim3(a.T), dim3(kMlThreads), lds, stream>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_choose(const MlArgs& a, hipStream_t stream) {
+  if (a.E <= 128) return launch_choose_t<2>(a, stream);
+  if (a.E <= 256) return launch_choose_t<4>(a, stream);
+  if (a.E <= 512) return launch_choose_t<8>(a, stream);
+  return launch_choose_t<16>(a, stream);
+}
+
 template <bool HALF>
 hipError_t launch_router(const MlArgs& a, hipStream_t stream) {
   // as few rounds as 1024 threads allow, and no more threads than they need
@@ -971,7 +1045,7 @@ hipError_t launch_router(const MlArgs& a, hipStream_t stream) {
 
 template <int GS, int KU>
 hipError_t launch_gate_up(const MlArgs& a, hipStream_t stream) {
-  const size_t lds = gate_up_front(a.E) + ml_plan_bytes(a.most, a.E);
+  const size_t lds = gate_up_front(a.T, a.E) + ml_plan_bytes(a.most, a.E);
   auto* kernel = &gate_up_kernel<GS, KU>;
   const hipError_t e = with_lds(kernel, lds);
   if (e != hipSuccess) return e;
@@ -999,6 +1073,10 @@ hipError_t launch_moe_layer_g(const MlArgs& a, bool half, hipStream_t stream) {
   using U = MlUnit<GS>;
   hipError_t e = half ? launch_router<true>(a, stream) : launch_router<false>(a, stream);
   if (e != hipSuccess) return e;
+  if (!choose_inside(a.T, a.E)) {
+    e = launch_choose(a, stream);
+    if (e != hipSuccess) return e;
+  }
   constexpr int kPer = U::K / 128;
   const int held = ((a.H / GS + U::G - 1) / U::G + kMlWaves - 1) / kMlWaves * kPer;  // 128s of K per wave
   if (held <= 2)
