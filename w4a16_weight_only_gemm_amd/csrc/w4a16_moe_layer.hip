@@ -30,6 +30,7 @@
 
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 
 #include "w4a16_device.h"
 #include "w4a16_epilogue.h"
@@ -44,8 +45,7 @@ constexpr int kMlTokens = W4A16_MOE_LAYER_MAX_TOKENS;
 constexpr int kMlMaxK = W4A16_ROUTE_MAX_TOP_K;
 constexpr int kMlWaves = 8;
 constexpr int kMlThreads = 64 * kMlWaves;
-constexpr int kMlMaxNB = 8;            // column blocks of a workgroup of down_kernel
-constexpr int kMlInnerBytes = 32 * 1024;  // inner rows that are held in LDS, at most
+constexpr int kMlMaxNB = 4;            // column blocks of a workgroup of down_kernel
 constexpr int kMlRouterThreads = 1024;  // at most
 constexpr int kMlPartFloats = 256;     // a 16 x 16 part
 
@@ -137,10 +137,35 @@ __global__ __launch_bounds__(kMlRouterThreads) void router_kernel(const MlArgs a
         acc[t] = __builtin_fma(static_cast<double>(xv), w[j], acc[t]);
       }
   }
+  // Sums over the wave. With 16 tokens every step within a row of 16 lanes halves the
+  // tokens a lane holds: it hands over the half that is its partner's and adds what it is
+  // given, 17 additions instead of 112. The partners mirror 16 lanes, then 8, then swap
+  // pairs, then neighbours: each agrees with the lane in all bits that were used before,
+  // so lane l is left with token l % 16 of its row.
+  if constexpr (TB == 16) {
+    auto step = [&](auto half_, auto ctrl_, int bit) {
+      constexpr int HALF_T = half_.value, CTRL = ctrl_.value;
+      const bool upper = lane >> bit & 1;
 #pragma unroll
-  for (int t = 0; t < TB; ++t) {
-    const double s = wave_sum_of(acc[t]);
-    if (lane == 0) part[wave][t] = s;
+      for (int i = 0; i < HALF_T; ++i) {
+        const double keep = upper ? acc[i + HALF_T] : acc[i], give = upper ? acc[i] : acc[i + HALF_T];
+        acc[i] = keep + dpp_of<CTRL, 0xF>(give);
+      }
+    };
+    using std::integral_constant;
+    step(integral_constant<int, 8>{}, integral_constant<int, 0x140>{}, 3);  // row_mirror
+    step(integral_constant<int, 4>{}, integral_constant<int, 0x141>{}, 2);  // row_half_mirror
+    step(integral_constant<int, 2>{}, integral_constant<int, 0x4E>{}, 1);   // quad_perm [2,3,0,1]
+    step(integral_constant<int, 1>{}, integral_constant<int, 0xB1>{}, 0);   // quad_perm [1,0,3,2]
+    acc[0] += __shfl_xor(acc[0], 16);
+    acc[0] += __shfl_xor(acc[0], 32);
+    if (lane < 16) part[wave][lane] = acc[0];
+  } else {
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      const double s = wave_sum_of(acc[t]);
+      if (lane == 0) part[wave][t] = s;
+    }
   }
   __syncthreads();
   if (tid < a.T) {
@@ -778,18 +803,18 @@ __global__ __launch_bounds__(kMlThreads) void gate_up_kernel(const MlArgs a) {
 }
 
 // NB: column blocks of a workgroup, which share the loads of its inner rows; AHEAD: units
-// of them a wave has on the way. INNER: the inner rows fit LDS (inner_bytes), and the long
-// sum the units on the way: nothing is split.
-template <int GS, int NB, int AHEAD, bool INNER>
-__global__ __launch_bounds__(kMlThreads) void down_kernel(const MlArgs a, int most_splits, int inner_bytes) {
+// of them a wave has on the way. 4 and 2: 4 blocks, 3 and 4 units and 5 blocks, 2 units
+// took up to 1.5 us more at 1, 3, 4 and 16 tokens. For one token of 8 experts, inner rows
+// through LDS, 2 blocks and all of a wave's 8 units on the way without splits: the same.
+template <int GS, int NB, int AHEAD>
+__global__ __launch_bounds__(kMlThreads) void down_kernel(const MlArgs a, int most_splits) {
   using U = MlUnit<GS>;
   extern __shared__ __attribute__((aligned(16))) unsigned char ml_lds[];
   __shared__ int last_flag;
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int c16 = lane & 15, lg = lane >> 4;
   float* const red = reinterpret_cast<float*>(ml_lds);  // [waves][NB][4][64]
-  unsigned char* const inner = ml_lds + kMlWaves * NB * 1024;  // INNER: [T][top_k][I]
-  const MlTables tb(ml_lds + kMlWaves * NB * 1024 + (INNER ? inner_bytes : 0), a.most);
+  const MlTables tb(ml_lds + kMlWaves * NB * 1024, a.most);
   const bf16x8 bias = bias_operand();
   const int groups = a.I / GS, units = (groups + U::G - 1) / U::G;  // of one expert
   const int blocks = a.H / 16;
@@ -806,22 +831,14 @@ __global__ __launch_bounds__(kMlThreads) void down_kernel(const MlArgs a, int mo
   }
   const uint32_t h_bytes = static_cast<uint32_t>(a.T * a.top_k) * a.I * 2;
   const __amdgpu_buffer_rsrc_t rh = make_rsrc(a.h, h_bytes);
-  constexpr int kPieces = INNER ? kMlInnerBytes / (16 * kMlThreads) : 1;
-  u32x4 held[kPieces];  // the inner rows on their way to LDS
-  if constexpr (INNER) {
-#pragma unroll
-    for (int p = 0; p < kPieces; ++p)
-      held[p] = __builtin_amdgcn_raw_buffer_load_b128(rh, (p * kMlThreads + tid) * 16, 0, 0);
-  }
   // Value i of the tile: block i / 256, row 4 (lane / 16) + i / 64 % 4 and column lane %
   // 16 of it, lane = i % 64. Whether there is such a value, and what is added to it.
   auto value_at = [&](int i, int& t, int& col) {
     t = 4 * ((i & 63) >> 4) + (i >> 6 & 3);
     col = (b0 + (i >> 8)) * 16 + (i & 15);
-    return t < a.T && col < a.H;
+    return i < NB * 256 && t < a.T && col < a.H;
   };
-  constexpr int kValues = NB * 256 / kMlThreads;  // a thread's
-  static_assert(kValues * kMlThreads == NB * 256, "whole threads");
+  constexpr int kValues = (NB * 256 + kMlThreads - 1) / kMlThreads;  // a thread's
   uint16_t base[kValues];
 #pragma unroll
   for (int j = 0; j < kValues; ++j) {
@@ -835,7 +852,7 @@ __global__ __launch_bounds__(kMlThreads) void down_kernel(const MlArgs a, int mo
 
   const int all = tb.plan->active * units;  // units of the long sum
   // as many parts as leave every wave a unit
-  const int splits = INNER ? 1 : max(1, min(most_splits, all / kMlWaves));
+  const int splits = max(1, min(most_splits, all / kMlWaves));
   if (split >= splits) return;
   // of one expert
   const uint32_t words = static_cast<uint32_t>(blocks) * groups * 64 * U::WPL;
@@ -887,37 +904,14 @@ __global__ __launch_bounds__(kMlThreads) void down_kernel(const MlArgs a, int mo
         s.h.d[g * U::WPL + w] = __builtin_amdgcn_raw_buffer_load_b128(rh, at, 16 * w, 0);
     }
   };
-  // the same from LDS, where any row stands for those of other tokens
-  auto read_inner = [&](Stage& s) {
-    const bool mine = tb.mask[s.at] >> c16 & 1;
-    const uint32_t slot = mine ? c16 * a.top_k + tb.place[s.at * 16 + c16] : 0;
-#pragma unroll
-    for (int g = 0; g < U::G; ++g) {
-      const int grp = min(s.u * U::G + g, groups - 1);
-#pragma unroll
-      for (int w = 0; w < U::WPL; ++w)
-        s.h.d[g * U::WPL + w] =
-            *reinterpret_cast<const u32x4*>(inner + (slot * a.I + grp * GS + (lg * U::WPL + w) * 8) * 2);
-    }
-  };
 #pragma unroll
   for (int p = 0; p < AHEAD; ++p) load_weights(ds[p]);
-  if constexpr (INNER) {
 #pragma unroll
-    for (int p = 0; p < kPieces; ++p)
-      if ((p * kMlThreads + tid) * 16 < static_cast<int>(h_bytes))
-        *reinterpret_cast<u32x4*>(inner + (p * kMlThreads + tid) * 16) = held[p];
-    lds_barrier();
-  }
-  if constexpr (!INNER) {
-#pragma unroll
-    for (int p = 0; p < AHEAD; ++p) load_inner(ds[p]);
-  }
+  for (int p = 0; p < AHEAD; ++p) load_inner(ds[p]);
   f32x4 y[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) y[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto unit = [&](Stage& s) {
-    if constexpr (INNER) read_inner(s);
+  auto unit = [&](const Stage& s) {
     const f32x4 wt = *reinterpret_cast<const f32x4*>(tb.weight + s.at * 16 + 4 * lg);
     const int live = static_cast<uint16_t>(tb.mask[s.at]) >> (4 * lg);
 #pragma unroll
@@ -940,18 +934,12 @@ __global__ __launch_bounds__(kMlThreads) void down_kernel(const MlArgs a, int mo
       }
     }
   };
-  if constexpr (INNER) {
+  for (int k = 0; k < n; k += AHEAD) {
 #pragma unroll
-    for (int p = 0; p < AHEAD; ++p)
-      if (p < n) unit(ds[p]);
-  } else {
-    for (int k = 0; k < n; k += AHEAD) {
-#pragma unroll
-      for (int p = 0; p < AHEAD; ++p) {
-        if (k + p < n) unit(ds[p]);
-        load_weights(ds[p]);
-        load_inner(ds[p]);
-      }
+    for (int p = 0; p < AHEAD; ++p) {
+      if (k + p < n) unit(ds[p]);
+      load_weights(ds[p]);
+      load_inner(ds[p]);
     }
   }
 
@@ -1055,16 +1043,16 @@ hipError_t launch_gate_up(const MlArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int GS, int NB, int AHEAD, bool INNER>
+template <int GS, int NB, int AHEAD>
 hipError_t launch_down(const MlArgs& a, hipStream_t stream) {
-  const int inner = INNER ? a.T * a.top_k * a.I * 2 : 0;
-  const size_t lds = static_cast<size_t>(kMlWaves) * NB * 1024 + inner + ml_plan_bytes(a.most, a.E);
-  auto* kernel = &down_kernel<GS, NB, AHEAD, INNER>;
+  static_assert(NB <= kMlMaxNB, "room for the parts");
+  const size_t lds = static_cast<size_t>(kMlWaves) * NB * 1024 + ml_plan_bytes(a.most, a.E);
+  auto* kernel = &down_kernel<GS, NB, AHEAD>;
   const hipError_t e = with_lds(kernel, lds);
   if (e != hipSuccess) return e;
   const int columns = (a.H / 16 + NB - 1) / NB;
-  const int splits = INNER || columns >= kModelCUs ? 1 : kModelCUs / columns;
-  kernel<<<dim3(columns * splits), dim3(kMlThreads), lds, stream>>>(a, splits, inner);
+  const int splits = columns < kModelCUs ? kModelCUs / columns : 1;
+  kernel<<<dim3(columns * splits), dim3(kMlThreads), lds, stream>>>(a, splits);
   return hipGetLastError();
 }
 
@@ -1087,17 +1075,12 @@ hipError_t launch_moe_layer_g(const MlArgs& a, bool half, hipStream_t stream) {
     e = launch_gate_up<GS, kPer == 1 ? 5 : 0>(a, stream);
   else if (held <= 6)
     e = launch_gate_up<GS, 6 / kPer>(a, stream);
+  else if (held <= 8 && GS >= 128)  // groups of 32 and 64 and their scales would spill
+    e = launch_gate_up<GS, GS >= 128 ? 8 / kPer : 0>(a, stream);
   else
     e = launch_gate_up<GS, 0>(a, stream);
   if (e != hipSuccess) return e;
-  // The long sum of few active experts is on its way as a whole, and their inner rows
-  // fit LDS; else it is split and streamed.
-  constexpr int kShort = U::F == 4 ? 8 : 4;
-  const int units = (a.I / GS + U::G - 1) / U::G;
-  if (static_cast<long long>(a.most) * units <= kMlWaves * kShort &&
-      static_cast<long long>(a.T) * a.top_k * a.I * 2 <= kMlInnerBytes)
-    return launch_down<GS, 2, kShort, true>(a, stream);
-  return launch_down<GS, 4, U::F == 4 ? 2 : 1, false>(a, stream);
+  return launch_down<GS, 4, U::F == 4 ? 2 : 1>(a, stream);
 }
 
 }  // namespace
