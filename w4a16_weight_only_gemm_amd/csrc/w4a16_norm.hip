@@ -50,18 +50,50 @@ __device__ __forceinline__ u32x4 to_bf16(const Piece& p) {
   return o;
 }
 
-// Eight floats of a row, or the first `left` of them, from any address of a float.
+// Where a thread's p-th piece of a row lies. The last piece of a row whose length is no
+// multiple of 8 is read as the row's last 8 columns and moved down by those that are not
+// its own, so that no load is a loop over columns.
+struct Span {
+  int at;     // first column read
+  int shift;  // columns read in front of the piece
+  int left;   // columns of the piece, 8 and more: all; 0 and less: there is none
+};
+
+__device__ __forceinline__ u32x4 moved_down(u32x4 v, int shift) {
+  if (shift & 4) v = u32x4{v[2], v[3], 0u, 0u};
+  if (shift & 2) v = u32x4{v[1], v[2], v[3], 0u};
+  if (shift & 1) v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+  return v;
+}
+
+// A piece as loaded, zeros where there is none. Unaligned addresses as in store_piece.
+typedef uint32_t half_piece __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32_quad __attribute__((ext_vector_type(4), aligned(4)));
-__device__ __forceinline__ Piece load_f32(gptr<const float> x, int left) {
+template <bool TAIL>
+__device__ __forceinline__ u32x4 load_bf16(gptr<const uint16_t> row, const Span& s) {
+  u32x4 v = *reinterpret_cast<gptr<const half_piece>>(row + s.at);
+  if constexpr (TAIL) v = moved_down(v, s.shift);
+  if (s.left <= 0) v = u32x4{0u, 0u, 0u, 0u};
+  return v;
+}
+template <bool TAIL>
+__device__ __forceinline__ Piece load_f32(gptr<const float> row, const Span& s) {
+  const f32x4 lo = *reinterpret_cast<gptr<const f32_quad>>(row + s.at);
+  const f32x4 hi = *reinterpret_cast<gptr<const f32_quad>>(row + s.at + 4);
   Piece p;
-  if (left >= 8) {
-    const f32x4 lo = *reinterpret_cast<gptr<const f32_quad>>(x);
-    const f32x4 hi = *reinterpret_cast<gptr<const f32_quad>>(x + 4);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) p.v[j] = j < 4 ? lo[j % 4] : hi[j % 4];
-  } else {
+  for (int j = 0; j < 8; ++j) p.v[j] = j < 4 ? lo[j % 4] : hi[j % 4];
+  if constexpr (TAIL) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) p.v[j] = j < left ? x[j] : 0.f;
+    for (int by = 4; by; by /= 2)
+      if (s.shift & by) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p.v[j] = j + by < 8 ? p.v[j + by] : 0.f;
+      }
+  }
+  if (s.left <= 0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p.v[j] = 0.f;
   }
   return p;
 }
@@ -113,8 +145,11 @@ struct RowJoin {
 };
 
 // P: pieces per thread. A row's pieces go round its threads, so that a wave's loads
-// are contiguous.
-template <int P, int L, bool BLOCK>
+// are contiguous. TAIL: N is no multiple of 8 (and at least 8).
+// Only y is asked for in front of the first sum. Asking for everything there costs
+// registers, and waves that would hide the waits more cheaply: 2048 rows of 2741, layer
+// norms on both sides and a gate 22.1 against 17.3 us.
+template <int P, int L, bool BLOCK, bool TAIL>
 __global__ __launch_bounds__(BLOCK ? 64 * kNormMaxWaves : 256) void norm_kernel(const NormArgs args) {
   const w4a16_norm_args& a = args.a;
   const int N = args.N;
@@ -129,19 +164,27 @@ __global__ __launch_bounds__(BLOCK ? 64 * kNormMaxWaves : 256) void norm_kernel(
   const float n = static_cast<float>(N);  // sums are divided: a constant row's mean is its value
   const bool layer = a.kind == W4A16_NORM_LAYER;
   const float one = a.unit_offset ? 1.f : 0.f;
-  auto left_of = [&](int p) { return N - 8 * (mine + p * per); };
-  auto at_of = [&](int p) { return 8 * (mine + p * per); };
-  auto vector = [&](const void* ptr, int p) {  // bf16 [N]
-    return bf16_piece(load_piece(to_global(static_cast<const uint16_t*>(ptr)) + at_of(p), left_of(p)));
-  };
+  const bool wide = a.residual_type == W4A16_RESIDUAL_F32;
+  Span span[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int at = 8 * (mine + p * per);
+    span[p].at = min(at, N - 8);
+    span[p].shift = min(at - span[p].at, 7);
+    span[p].left = N - at;
+  }
   auto bf16_row = [&](const void* ptr, long long r, int p) {
-    return bf16_piece(load_piece(to_global(static_cast<const uint16_t*>(ptr)) + r * N + at_of(p), left_of(p)));
+    return load_bf16<TAIL>(to_global(static_cast<const uint16_t*>(ptr)) + r * N, span[p]);
   };
+  auto first_of = [&](int p) { return span[p].at + span[p].shift; };  // where there is a piece
+
+  const u32x4 none = {0u, 0u, 0u, 0u};
+  const bool next = a.x || a.xq;
 
   Piece v[P];
   // (v - mean) / sqrt(mean square + eps) * weight + bias, in place; columns past N
   // hold zeros and stay out of the sums
-  auto normalise = [&](const void* weight, const void* bias) {
+  auto normalise = [&](const void* w, const void* b) {
     if (layer) {
       float s = 0.f;
 #pragma unroll
@@ -152,7 +195,8 @@ __global__ __launch_bounds__(BLOCK ? 64 * kNormMaxWaves : 256) void norm_kernel(
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[p].v[j] = j < left_of(p) ? v[p].v[j] - mean : 0.f;
+        for (int j = 0; j < 8; ++j)
+          v[p].v[j] = (TAIL ? j < span[p].left : span[p].left > 0) ? v[p].v[j] - mean : 0.f;
     }
     float s = 0.f;
 #pragma unroll
@@ -162,69 +206,53 @@ __global__ __launch_bounds__(BLOCK ? 64 * kNormMaxWaves : 256) void norm_kernel(
     const float r = 1.f / sqrtf(sum(s) / n + a.eps);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      if (left_of(p) <= 0) continue;
-      Piece w, b;
-      if (weight) w = vector(weight, p);
-      if (bias) b = vector(bias, p);
+      const Piece wp = bf16_piece(w ? bf16_row(w, 0, p) : none), bp = bf16_piece(b ? bf16_row(b, 0, p) : none);
+      if (span[p].left <= 0) continue;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         float x = v[p].v[j] * r;
-        if (weight) x *= w.v[j] + one;
-        if (bias) x += j < left_of(p) ? b.v[j] : 0.f;
+        if (w) x *= wp.v[j] + one;
+        if (b) x += bp.v[j];  // 0 past N
         v[p].v[j] = x;
       }
     }
   };
 
 #pragma unroll
-  for (int p = 0; p < P; ++p) {
-    if (left_of(p) > 0 && a.y) {
-      v[p] = bf16_row(a.y, row, p);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[p].v[j] = 0.f;
-    }
-  }
+  for (int p = 0; p < P; ++p) v[p] = bf16_piece(a.y ? bf16_row(a.y, row, p) : none);
   if (a.y) {
     if (a.post_norm) normalise(a.post_weight, a.post_bias);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      if (left_of(p) <= 0) continue;
-      if (a.gate) {
-        const Piece g = bf16_row(a.gate, row / a.gate_rows, p);
+      const Piece g = bf16_piece(a.gate ? bf16_row(a.gate, row / a.gate_rows, p) : none);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[p].v[j] *= g.v[j];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[p].v[j] *= a.scale;
+      for (int j = 0; j < 8; ++j) v[p].v[j] = (a.gate ? v[p].v[j] * g.v[j] : v[p].v[j]) * a.scale;
     }
   }
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    if (left_of(p) <= 0) continue;
-    const size_t at = static_cast<size_t>(row) * N + at_of(p);
-    const bool wide = a.residual_type == W4A16_RESIDUAL_F32;
     if (a.residual) {
-      const Piece r = wide ? load_f32(to_global(static_cast<const float*>(a.residual)) + at, left_of(p))
-                           : bf16_row(a.residual, row, p);
+      const Piece res = wide ? load_f32<TAIL>(to_global(static_cast<const float*>(a.residual)) + row * N, span[p])
+                             : bf16_piece(bf16_row(a.residual, row, p));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[p].v[j] += r.v[j];
+      for (int j = 0; j < 8; ++j) v[p].v[j] += res.v[j];
     }
-    if (a.residual_out) {
+    if (a.residual_out && span[p].left > 0) {
+      const size_t at = static_cast<size_t>(row) * N + first_of(p);
       if (wide)
-        store_f32(to_global(static_cast<float*>(a.residual_out)) + at, v[p], left_of(p));
+        store_f32(to_global(static_cast<float*>(a.residual_out)) + at, v[p], span[p].left);
       else
-        store_piece(to_global(static_cast<uint16_t*>(a.residual_out)) + at, to_bf16(v[p]), left_of(p));
+        store_piece(to_global(static_cast<uint16_t*>(a.residual_out)) + at, to_bf16(v[p]), span[p].left);
     }
   }
-  if (!a.x && !a.xq) return;
+  if (!next) return;
   normalise(a.weight, a.bias);
   if (a.x) {
 #pragma unroll
     for (int p = 0; p < P; ++p)
-      if (left_of(p) > 0)
-        store_piece(to_global(static_cast<uint16_t*>(a.x)) + static_cast<size_t>(row) * N + at_of(p),
-                    to_bf16(v[p]), left_of(p));
+      if (span[p].left > 0)
+        store_piece(to_global(static_cast<uint16_t*>(a.x)) + static_cast<size_t>(row) * N + first_of(p),
+                    to_bf16(v[p]), span[p].left);
     return;
   }
   // The codes and scale of w4a8_quantize, of values that were not rounded before.
@@ -238,7 +266,7 @@ __global__ __launch_bounds__(BLOCK ? 64 * kNormMaxWaves : 256) void norm_kernel(
   if (mine == 0) to_global(a.sx)[row] = big / 127.f;
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    if (left_of(p) <= 0) continue;
+    if (span[p].left <= 0) continue;
     uint32_t c[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -250,8 +278,56 @@ __global__ __launch_bounds__(BLOCK ? 64 * kNormMaxWaves : 256) void norm_kernel(
     // half a 16-block: byte j holds offset 0,4,1,5,2,6,3,7
     const u32x2 o = {c[0] | c[4] << 8 | c[1] << 16 | c[5] << 24, c[2] | c[6] << 8 | c[3] << 16 | c[7] << 24};
     *reinterpret_cast<gptr<u32x2>>(to_global(static_cast<uint8_t*>(a.xq)) + static_cast<size_t>(row) * N +
-                                   at_of(p)) = o;
+                                   first_of(p)) = o;
   }
+}
+
+// Rows of fewer than 8 columns: a thread a row.
+__global__ __launch_bounds__(64) void norm_short_kernel(const NormArgs args) {
+  const w4a16_norm_args& a = args.a;
+  const int N = args.N;
+  const long long row = static_cast<long long>(blockIdx.x) * 64 + threadIdx.x;
+  if (row >= args.T) return;
+  const float n = static_cast<float>(N);
+  const bool wide = a.residual_type == W4A16_RESIDUAL_F32;
+  auto bf16_at = [](const void* p, long long i) { return bf16_bits_to_f32(to_global(static_cast<const uint16_t*>(p))[i]); };
+  float v[7];
+  auto normalise = [&](const void* w, const void* b) {
+    float mean = 0.f, s = 0.f;
+    if (a.kind == W4A16_NORM_LAYER) {
+      for (int j = 0; j < 7; ++j) mean += j < N ? v[j] : 0.f;
+      mean /= n;
+    }
+    for (int j = 0; j < 7; ++j) {
+      v[j] -= mean;
+      s += j < N ? v[j] * v[j] : 0.f;
+    }
+    const float r = 1.f / sqrtf(s / n + a.eps);
+    for (int j = 0; j < 7; ++j) {
+      if (j >= N) continue;
+      v[j] *= r;
+      if (w) v[j] *= bf16_at(w, j) + (a.unit_offset ? 1.f : 0.f);
+      if (b) v[j] += bf16_at(b, j);
+    }
+  };
+  for (int j = 0; j < 7; ++j) v[j] = a.y && j < N ? bf16_at(a.y, row * N + j) : 0.f;
+  if (a.y && a.post_norm) normalise(a.post_weight, a.post_bias);
+  for (int j = 0; j < 7; ++j) {
+    if (j >= N) continue;
+    if (a.y) v[j] = (a.gate ? v[j] * bf16_at(a.gate, row / a.gate_rows * N + j) : v[j]) * a.scale;
+    if (a.residual)
+      v[j] += wide ? to_global(static_cast<const float*>(a.residual))[row * N + j] : bf16_at(a.residual, row * N + j);
+    if (a.residual_out) {
+      if (wide)
+        to_global(static_cast<float*>(a.residual_out))[row * N + j] = v[j];
+      else
+        to_global(static_cast<uint16_t*>(a.residual_out))[row * N + j] = f32_to_bf16_bits(v[j]);
+    }
+  }
+  if (!a.x) return;  // codes need 16 columns
+  normalise(a.weight, a.bias);
+  for (int j = 0; j < 7; ++j)
+    if (j < N) to_global(static_cast<uint16_t*>(a.x))[row * N + j] = f32_to_bf16_bits(v[j]);
 }
 
 template <int P, int L, bool BLOCK>
@@ -260,8 +336,9 @@ hipError_t launch_norm_t(const NormArgs& args, int threads, hipStream_t stream) 
   if (blocks * threads > 0xFFFFFFFFLL) return hipErrorNotSupported;
   NormArgs copy = args;
   void* kargs[] = {&copy};
-  return hipLaunchKernel(reinterpret_cast<const void*>(&norm_kernel<P, L, BLOCK>),
-                         dim3(static_cast<unsigned>(blocks)), dim3(threads), kargs, 0, stream);
+  const void* fn = args.N % 8 != 0 ? reinterpret_cast<const void*>(&norm_kernel<P, L, BLOCK, true>)
+                                   : reinterpret_cast<const void*>(&norm_kernel<P, L, BLOCK, false>);
+  return hipLaunchKernel(fn, dim3(static_cast<unsigned>(blocks)), dim3(threads), kargs, 0, stream);
 }
 
 template <int P>
@@ -275,11 +352,23 @@ hipError_t launch_norm_block(const NormArgs& args, int pieces, hipStream_t strea
 hipError_t launch_norm(const w4a16_norm_args& a, int T, int N, hipStream_t stream) {
   const NormArgs args = {a, T, N};
   const int pieces = (N + 7) / 8;
+  if (N < 8) {
+    NormArgs copy = args;
+    void* kargs[] = {&copy};
+    return hipLaunchKernel(reinterpret_cast<const void*>(&norm_short_kernel), dim3((T - 1) / 64 + 1), dim3(64), kargs, 0,
+                           stream);
+  }
   if (pieces <= 16) return launch_norm_t<1, 16, false>(args, 256, stream);
   if (pieces <= 32) return launch_norm_t<1, 32, false>(args, 256, stream);
   if (pieces <= 64) return launch_norm_t<1, 64, false>(args, 256, stream);
-  if (pieces <= 64 * kNormMaxWaves) return launch_norm_block<1>(args, pieces, stream);
+  // Two pieces a thread halve the waves that a sum has to meet; with few rows, which do
+  // not fill the card, one a thread is sooner done (us, one / two / four): 64 rows of 5120
+  // with post norm and codes 11.3 / 12.1 / 13.9, 500 of 4096 7.1 / 7.6 / 10.6; 2048 of
+  // 2741 with layer norms 20.1 / 17.4 / 22.1, 4000 of 4096 with post norm 32.6 / 29.9 / 35.7.
+  if (args.T < 1024 && pieces <= 64 * kNormMaxWaves) return launch_norm_block<1>(args, pieces, stream);
   if (pieces <= 2 * 64 * kNormMaxWaves) return launch_norm_block<2>(args, pieces, stream);
+  // (1000 rows of 17408: 35.5 us with three, 46.3 with four)
+  if (pieces <= 3 * 64 * kNormMaxWaves) return launch_norm_block<3>(args, pieces, stream);
   if (pieces <= 4 * 64 * kNormMaxWaves) return launch_norm_block<4>(args, pieces, stream);
   return launch_norm_block<8>(args, pieces, stream);
 }
