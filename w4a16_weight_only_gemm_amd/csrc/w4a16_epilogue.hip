@@ -54,7 +54,7 @@ __global__ __launch_bounds__(kLgThreads, 1) void tile_epilogue_kernel(const Gemm
   zero(acc);
   const int kt = (e.G + C::T - 1) / C::T;
   if constexpr (D == 1)
-    e.kloop(acc, 0, kt);
+    e.kloop_spread(acc, 0, kt);  // 1024 rows, 5120 x 34816, gated: 371 us, with kloop 390
   else
     e.template kloop_deep<D>(acc, 0, kt);
 
@@ -149,8 +149,11 @@ hipError_t launch_tile_epilogue_g(const GemmArgs& a, const Epilogue& ep, int row
 
 // --------------------------------------------------------------- few rows
 
-// The form for a gated product: w4a16_gemm's where its column blocks come in
-// pairs, else the nearest that has pairs.
+// The form for a gated product: w4a16_gemm's where its column blocks come in pairs,
+// else one that has pairs. For the 4-wave forms of wide N that is 6 blocks while that
+// gives every compute unit a workgroup, else 2 (us of 2, 4 and 6 blocks at 5120 x 34816: 1
+// row 24.0, 21.8, 20.8, 16 rows 29.1, 27.4, 23.7; at 2560 x 17408: 1 row 8.1, 9.9, 10.5, 16
+// rows 10.2, 10.4, 10.7).
 int gated_form(int M, int N, int K, int group) {
   const int f = plain_form(M, N, K, group);
   const size_t staged = static_cast<size_t>(M < 16 ? M : 16) * (static_cast<size_t>(K) + 8) * 2 +
@@ -158,18 +161,21 @@ int gated_form(int M, int N, int K, int group) {
   switch (f) {
     case kOne16Staged: return staged <= kPlainLdsLimit ? kDeepStaged : kTwo16;
     case kOne16: return kTwo16;
-    case kXs1x3w4: return kXs1x4w4;
-    case kXs1x5w4: return kXs1x6w4;
+    case kXs1x3w4: case kXs1x5w4: return N / 32 / 3 >= kModelCUs ? kXs1x6w4 : kXs1x2w4;
     case kXs1x5: return kXs1x4;
-    case kXs2x3: case kXs2x5: case kXs2x5w4: return kXs2x4;
+    case kXs2x3: case kXs2x5: return kXs2x4;
     default: return f;
   }
 }
 
 template <int GS>
 hipError_t launch_epilogue_g(const GemmArgs& a, const Epilogue& ep, bool gated, hipStream_t stream) {
-  if (choose_path(a.M, a.N, a.K, GS) == W4A16_PATH_LARGE && large_runs(a.N, a.K, GS)) {
-    if constexpr (GS <= 128) {
+  if constexpr (GS <= 128) {
+    // The 4-wave form of 2 x 5 blocks has no twin in pairs as good as the tiles (2 x 4 blocks
+    // at 24 rows, 5120 x 34816: 36.2 us, tiles 32.1).
+    const bool tiles = choose_path(a.M, a.N, a.K, GS) == W4A16_PATH_LARGE ||
+                       (gated && a.M <= kPlainMaxRows && plain_form(a.M, a.N, a.K, GS) == kXs2x5w4);
+    if (tiles && large_runs(a.N, a.K, GS)) {
       int rows = 128;
       tile_estimate_us(a.M, a.N, a.K, GS, &rows);
       return gated ? launch_tile_epilogue_g<GS, kEpiGated>(a, ep, rows, stream)

@@ -428,8 +428,8 @@ enum PlainForm : int {
   kOp4x4,        // 4 x 4, 4 waves
   // gated epilogues only, whose column blocks come in pairs
   kTwo16,        // 1 x 2, 16 waves
-  kXs1x4w4,      // 1 x 4, 4 waves, XS
   kXs1x6w4,      // 1 x 6, 4 waves, XS
+  kXs1x2w4,      // 1 x 2, 4 waves, XS
   kPlainForms
 };
 
@@ -440,7 +440,7 @@ constexpr PlainFormInfo kPlainFormInfo[kPlainForms] = {
     {1, 2, 4}, {1, 2, 4}, {1, 4, 4}, {1, 2, 16}, {1, 2, 8}, {1, 1, 16}, {1, 1, 16},
     {1, 2, 8}, {1, 4, 8}, {1, 5, 8}, {2, 2, 16}, {2, 3, 16}, {2, 4, 16}, {2, 5, 8}, {4, 4, 16},
     {1, 3, 4}, {1, 5, 4}, {2, 5, 4}, {1, 2, 8},
-    {2, 2, 4}, {2, 4, 4}, {4, 2, 4}, {4, 4, 4}, {1, 2, 16}, {1, 4, 4}, {1, 6, 4}};
+    {2, 2, 4}, {2, 4, 4}, {4, 2, 4}, {4, 4, 4}, {1, 2, 16}, {1, 6, 4}, {1, 2, 4}};
 
 // Launches a form. Forms of an odd number of column blocks, and at other groups
 // than 128 the XS forms, are not built for the kernels that cannot have them.
@@ -487,8 +487,8 @@ hipError_t launch_plain_form(int form, const GemmArgs& a, const Epilogue& ep, hi
   if constexpr (EPI == kEpiGated) {
     switch (form) {
       case kTwo16: return launch_plain_if<GS, EPI, 1, 2, 16, P1, false>(a, ep, s);
-      case kXs1x4w4: return launch_plain_if<GS, EPI, 1, 4, 4, 1, false, 1, true>(a, ep, s);
       case kXs1x6w4: return launch_plain_if<GS, EPI, 1, 6, 4, 1, false, 1, true>(a, ep, s);
+      case kXs1x2w4: return launch_plain_if<GS, EPI, 1, 2, 4, 1, false, 1, true>(a, ep, s);
       default: break;
     }
   }
