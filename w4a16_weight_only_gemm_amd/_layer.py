@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import struct
 
 from . import W4A16_OK, W4A16Error, _lib, _ptr, _stream, w4a16_qweight_bytes, w4a16_scales_bytes
 from ._moe import (_BF16, _F32, _I8, _I32, W4A16_ACT_NONE, W4A16_ACT_SWIGLU, W4A16_LOGITS_BF16,
@@ -57,8 +58,20 @@ for _name, (_res, _args) in LAYER_SIGNATURES.items():
     _fn.argtypes = _args
 
 
-def _address(struct):
-    return ctypes.addressof(struct) if struct is not None else None
+# The same structures as bytes: a call's own, made in a fraction of the time ctypes takes
+# (small calls are bound by the host).
+_PACK_EPILOGUE = struct.Struct("@PPfi0P").pack
+_PACK_MOE_LAYER = struct.Struct("@8if4iPPPPPP").pack
+_PACK_NORM = struct.Struct("@PiiPPPfiPPPPPPPiif0P").pack
+
+
+def _address(args):
+    return ctypes.addressof(args) if args is not None else None
+
+
+def _or_0(name: str, t, dtype, nbytes: int, dev: int) -> int:
+    """_at for a field of a packed structure, where an absent buffer is 0."""
+    return 0 if t is None else _at(name, t, dtype, nbytes, dev) or 0
 
 
 def gemm_epilogue_status(x, qweight, scales, epilogue: w4a16_epilogue | None, y, M, N, K, group,
@@ -84,11 +97,11 @@ def w4a16_gemm_epilogue(x, qweight, scales, y, M: int, N: int, K: int, group: in
     qb = sb = 0
     if N >= 0 and K >= 0 and group > 0 and group % 32 == 0 and K % group == 0:
         qb, sb = _packed_bytes(N, K, group)
-    ep = w4a16_epilogue(_at("bias", bias, _BF16, 2 * N, dev),
-                        _at("residual", residual, _BF16, 2 * M * out, dev), scale, act)
+    ep = _PACK_EPILOGUE(_or_0("bias", bias, _BF16, 2 * N, dev),
+                        _or_0("residual", residual, _BF16, 2 * M * out, dev), scale, act)
     rc = _lib.w4a16_gemm_epilogue(
         _at("x", x, _BF16, 2 * M * K, dev), _at("qweight", qweight, None, qb, dev),
-        _at("scales", scales, None, sb, dev), ctypes.addressof(ep),
+        _at("scales", scales, None, sb, dev), ep,
         _at("y", y, _BF16, 2 * M * out, dev), M, N, K, group, _on(stream, dev))
     if rc != W4A16_OK:
         raise W4A16Error(rc, "w4a16_gemm_epilogue")
@@ -117,16 +130,16 @@ def w4a16_norm(T: int, N: int, *, y=None, residual=None, residual_out=None, post
     stored, row, vec = _F32 if wide else _BF16, 2 * T * N, 2 * N
     full = 2 * row if wide else row
     gates = -(-T // gate_rows) if gate_rows > 0 else 0
-    args = w4a16_norm_args(
-        _at("y", y, _BF16, row, dev), 1 if post_norm else 0, gate_rows,
-        _at("post_weight", post_weight, _BF16, vec, dev),
-        _at("post_bias", post_bias, _BF16, vec, dev), _at("gate", gate, _BF16, gates * vec, dev),
-        scale, residual_type, _at("residual", residual, stored, full, dev),
-        _at("residual_out", residual_out, stored, full, dev),
-        _at("weight", weight, _BF16, vec, dev), _at("bias", bias, _BF16, vec, dev),
-        _at("x", x, _BF16, row, dev), _at("xq", xq, _I8, T * N, dev),
-        _at("sx", sx, _F32, 4 * T, dev), kind, 1 if unit_offset else 0, eps)
-    rc = _lib.w4a16_norm(ctypes.addressof(args), T, N, _on(stream, dev))
+    args = _PACK_NORM(
+        _or_0("y", y, _BF16, row, dev), 1 if post_norm else 0, gate_rows,
+        _or_0("post_weight", post_weight, _BF16, vec, dev),
+        _or_0("post_bias", post_bias, _BF16, vec, dev), _or_0("gate", gate, _BF16, gates * vec, dev),
+        scale, residual_type, _or_0("residual", residual, stored, full, dev),
+        _or_0("residual_out", residual_out, stored, full, dev),
+        _or_0("weight", weight, _BF16, vec, dev), _or_0("bias", bias, _BF16, vec, dev),
+        _or_0("x", x, _BF16, row, dev), _or_0("xq", xq, _I8, T * N, dev),
+        _or_0("sx", sx, _F32, 4 * T, dev), kind, 1 if unit_offset else 0, eps)
+    rc = _lib.w4a16_norm(args, T, N, _on(stream, dev))
     if rc != W4A16_OK:
         raise W4A16Error(rc, "w4a16_norm")
 
@@ -142,11 +155,6 @@ def moe_layer_status(layer: w4a16_moe_layer_args | None, x, live, base, out, ids
     return int(_lib.w4a16_moe_layer(_address(layer), _ptr(x), _ptr(live), _ptr(base), _ptr(out),
                                     _ptr(ids), _ptr(weights), T, _ptr(workspace), workspace_bytes,
                                     _stream(stream)))
-
-
-@functools.lru_cache(maxsize=256)
-def _route(*fields) -> w4a16_route_config:
-    return w4a16_route_config(*fields)
 
 
 def w4a16_moe_layer(x, router, gate_up, gate_up_scales, down, down_scales, out, ids, weights,
@@ -177,16 +185,16 @@ def w4a16_moe_layer(x, router, gate_up, gate_up_scales, down, down_scales, out, 
     if workspace_bytes is None:
         workspace_bytes = workspace.nbytes if isinstance(workspace, _Tensor) else 0
     row, places = 2 * T * hidden, 4 * T * top_k
-    args = w4a16_moe_layer_args(
-        _route(E, top_k, scoring, router_type, groups, groups_kept, group_top,
-               1 if renormalize else 0, scale),
-        router_type, hidden, width, group,
-        _at("router", router, _BF16 if half else _F32, (2 if half else 4) * E * hidden, dev),
-        _at("route_bias", route_bias, _F32, 4 * E, dev), _at("gate_up", gate_up, None, E * gb, dev),
-        _at("gate_up_scales", gate_up_scales, None, E * gs, dev),
-        _at("down", down, None, E * db, dev), _at("down_scales", down_scales, None, E * ds, dev))
+    args = _PACK_MOE_LAYER(
+        E, top_k, scoring, router_type, groups, groups_kept, group_top, 1 if renormalize else 0,
+        scale, router_type, hidden, width, group,
+        _or_0("router", router, _BF16 if half else _F32, (2 if half else 4) * E * hidden, dev),
+        _or_0("route_bias", route_bias, _F32, 4 * E, dev),
+        _or_0("gate_up", gate_up, None, E * gb, dev),
+        _or_0("gate_up_scales", gate_up_scales, None, E * gs, dev),
+        _or_0("down", down, None, E * db, dev), _or_0("down_scales", down_scales, None, E * ds, dev))
     rc = _lib.w4a16_moe_layer(
-        ctypes.addressof(args), _at("x", x, _BF16, row, dev), _at("live", live, _I32, 4 * T, dev),
+        args, _at("x", x, _BF16, row, dev), _at("live", live, _I32, 4 * T, dev),
         _at("base", base, _BF16, row, dev), _at("out", out, _BF16, row, dev),
         _at("ids", ids, _I32, places, dev), _at("weights", weights, _F32, places, dev), T,
         _at("workspace", workspace, None, workspace_bytes, dev), workspace_bytes, _on(stream, dev))
