@@ -109,12 +109,11 @@ typedef struct w4a16_norm_args {
  * With xq and sx instead of x: a = max |v|, sx[t] = a / 127, codes v * (127 / a)
  * rounded to the nearest integer (ties to even) in -127 .. 127; 0 and sx 0 for a
  * row of zeros. Inputs of rows that are written as codes must be finite.
- * A mean of squares is taken of the deviations themselves (two passes over the
- * row in registers). A mean of squares past fp32 is infinite, and its
- * row comes out as zeros (and biases), as the formula in fp32 has it.
- * Supported: T >= 0, 1 <= N <= W4A16_NORM_MAX_COLUMNS, for codes N % 16 == 0;
- * a grid of
- * fewer than 2^32 threads (else W4A16_ERR_UNSUPPORTED). y, gate, residual,
+ * The mean of squares of a layer norm is taken of the deviations themselves. A
+ * mean of squares past fp32 is infinite, and its row comes out as zeros (and
+ * biases), as the formula in fp32 has it.
+ * Supported: T >= 0, 1 <= N <= W4A16_NORM_MAX_COLUMNS, for codes N % 16 == 0; a
+ * grid of fewer than 2^32 threads (else W4A16_ERR_UNSUPPORTED). y, gate, residual,
  * residual_out, x and xq 16-byte aligned, the vectors 2-byte, sx 4-byte. Outputs
  * overlap no input (residual_out may be residual) and not each other. T == 0
  * launches nothing. At least one of y and residual, and one output, must be
@@ -165,11 +164,12 @@ size_t w4a16_moe_layer_workspace_bytes(int T, int experts, int top_k, int hidden
  *   ids  : device int32 [T][top_k]; weights : device f32 [T][top_k]
  *   workspace : w4a16_moe_layer_workspace_bytes(...) bytes
  * Supported: 0 <= T <= W4A16_MOE_LAYER_MAX_TOKENS, group in {32, 64, 128, 256},
- * hidden % group == 0, width % group == 0, one expert's packed matrix below 4 GB
- * (else W4A16_ERR_UNSUPPORTED; more tokens take w4a16_moe_route and the calls
- * behind it). x, router, the packed weights and scales, base and out 16-byte
- * aligned, workspace 256-byte, the rest 4-byte. T == 0 launches nothing. Two
- * launches on `stream`.
+ * hidden % group == 0, width % group == 0, one expert's packed matrix and the
+ * T * top_k inner rows below 4 GB (else W4A16_ERR_UNSUPPORTED; more tokens take
+ * w4a16_moe_route and the calls behind it). x, router, the packed weights and scales, base and out 16-byte
+ * aligned, workspace 256-byte, the rest 4-byte. T == 0 launches nothing. Three
+ * launches on `stream` for up to 64 experts, or one or two tokens of up to 256,
+ * else four. ids and weights are handed from one launch to the next.
  * Returns W4A16_OK, W4A16_ERR_INVALID_ARG (null pointer, bad field, workspace
  * too small), W4A16_ERR_UNSUPPORTED, W4A16_ERR_MISALIGNED or W4A16_ERR_LAUNCH.
  */

@@ -47,6 +47,18 @@ def test_structures_match_the_header(tmp_path):
     assert got == want
 
 
+def test_packed_structures_are_the_same():
+    """The bytes the calls pass, against the ctypes structures of the same values."""
+    from w4a16_weight_only_gemm_amd import _layer
+    assert _layer._PACK_EPILOGUE(1, 2, 0.5, 3) == bytes(w4.w4a16_epilogue(1, 2, 0.5, 3))
+    v = [11, 1, 2, 12, 13, 14, 0.25, 1, 15, 16, 17, 18, 19, 20, 21, 1, 1, 0.125]
+    assert _layer._PACK_NORM(*v) == bytes(w4.w4a16_norm_args(*v))
+    r = [8, 2, 1, 1, 4, 2, 2, 1, 1.5]
+    tail = [1, 256, 128, 32, 31, 32, 33, 34, 35, 36]
+    assert (_layer._PACK_MOE_LAYER(*r, *tail)
+            == bytes(w4.w4a16_moe_layer_args(w4.w4a16_route_config(*r), *tail)))
+
+
 def ep(bias=None, residual=None, scale=1.0, act=0):
     return w4.w4a16_epilogue(bias, residual, scale, act)
 
@@ -134,7 +146,8 @@ def test_moe_layer_refusals():
         assert st(layer(**{bad: B})) == MISALIGNED, bad
     assert st(layer(), T=17) == UNSUPPORTED
     for bad in (dict(hidden=0), dict(width=0), dict(group=0), dict(group=96), dict(hidden=192), dict(width=64),
-                dict(hidden=1 << 17, width=1 << 17), dict(width=2**30, hidden=128)):
+                dict(hidden=1 << 17, width=1 << 17), dict(width=2**30, hidden=128),
+                dict(hidden=32, width=1 << 27, group=32)):  # inner rows past 4 GB
         assert st(layer(**bad)) == UNSUPPORTED, bad
     need = w4.w4a16_moe_layer_workspace_bytes(4, 16, 4, 256, 128)
     assert need > 0 and st(layer(), n=need - 1) == INVALID

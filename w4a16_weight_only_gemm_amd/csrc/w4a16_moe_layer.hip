@@ -9,23 +9,23 @@
 // wave needs of the activations does not depend on the expert.
 //  * router_kernel: a workgroup per expert, products and sums in fp64 (a bf16 by f32
 //    product is exact there), so that the choice does not depend on an order of
-//    additions. It also clears the counters of the other kernel.
-//  * experts_kernel, one workgroup per compute unit:
-//    - every workgroup chooses the experts itself, from the logits, and lists those
-//      that are active;
-//    - gate and up: a wave owns a range of K and holds its tokens' activations of
-//      that range in registers, while the weights of one (expert, 16 gate and 16 up
-//      columns) after the other stream by, a whole task ahead. The waves' sums meet
-//      in LDS, where SwiGLU is formed;
-//    - down: the active experts' k ranges laid end to end are one long sum for every
-//      16 columns of the output, each expert's part weighted by its tokens' weights on
-//      the way. A workgroup takes a few column blocks of a part of it; the parts are
-//      added by the last workgroup to finish one, in their order, so results do not
-//      depend on timing.
-//    Between the two every workgroup waits for all inner rows, its first weights of
-//    down on their way meanwhile.
-// Bound by HBM from a few tokens on; at one token by the launches and by the chain
-// logits, choice, first weights.
+//    additions. It also clears down_kernel's counters.
+//  * choose_kernel: a workgroup per token chooses its experts from the logits, where that
+//    is not done by every workgroup of gate_up_kernel (choose_inside).
+//  * gate_up_kernel: a wave owns a range of K and holds its tokens' activations of that
+//    range in registers, while the weights of one (expert, 16 gate and 16 up columns)
+//    after the other stream by, a whole task ahead. The waves' sums meet in LDS, where
+//    SwiGLU is formed. 16 tokens of 128 experts, 5120 x 1024: 6.7 TB/s while it streams.
+//  * down_kernel: the active experts' k ranges laid end to end are one long sum for every
+//    16 columns of the output, each expert's part weighted by its tokens' weights on the
+//    way. A workgroup takes a few column blocks of an even part of it; the parts are
+//    added by the last workgroup to finish one, in their order, so results do not depend
+//    on timing.
+// Bound by HBM from a few tokens on (16 tokens: 113 us, 82 of them streaming); at one
+// token (27 us) by three launches' ramps and by the chain logits, choice, first
+// weights. Gate, up and down in one launch, whose workgroups wait for the inner rows with
+// down's first weights on their way, took 30 us there and 123 at 16 tokens: the rows'
+// way through memory and the polls behind the weights cost more than a launch.
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
@@ -593,8 +593,8 @@ __device__ __forceinline__ void load_unit(MlWeights<GS>& r, const MlMatrix& m, i
   const uint32_t wl = m.there ? lane * U::WPL * 4 : far, sl = m.there ? (lane & 14) * 2 : far;
 #pragma unroll
   for (int g = 0; g < U::G; ++g) {
-    const int at = tile + u * U::G + g;
-    const int wat = at * (256 * U::WPL);
+    const uint32_t at = tile + u * U::G + g;
+    const int wat = static_cast<int>(at * (256u * U::WPL));
     if constexpr (U::WPL >= 4) {
 #pragma unroll
       for (int q = 0; q < U::WPL / 4; ++q) {
@@ -609,7 +609,7 @@ __device__ __forceinline__ void load_unit(MlWeights<GS>& r, const MlMatrix& m, i
     } else {
       r.w[g] = __builtin_amdgcn_raw_buffer_load_b32(m.w, wl, wat, kOnce);
     }
-    r.s[g] = __builtin_amdgcn_raw_buffer_load_b32(m.s, sl, at * 32, 0);
+    r.s[g] = __builtin_amdgcn_raw_buffer_load_b32(m.s, sl, static_cast<int>(at * 32u), 0);
   }
 }
 
@@ -989,21 +989,21 @@ __global__ __launch_bounds__(kMlThreads) void down_kernel(const MlArgs a, int mo
 
 // ---------------------------------------------------------------- launches
 
-template <typename F>
-hipError_t with_lds(F* kernel, size_t lds) {
-  if (lds <= 64 * 1024) return hipSuccess;
-  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(lds));
+template <typename... Params, typename... Args>
+hipError_t launch(void (*kernel)(Params...), int grid, int threads, size_t lds, hipStream_t stream, Args... args) {
+  const void* fn = reinterpret_cast<const void*>(kernel);
+  if (lds >= 60 * 1024) {  // with the kernels' own variables past the 64 KB that need no leave
+    const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
+    if (e != hipSuccess) return e;
+  }
+  static_assert((std::is_same_v<Params, Args> && ...), "arguments are passed by address");
+  void* kargs[] = {&args...};
+  return hipLaunchKernel(fn, dim3(grid), dim3(threads), kargs, lds, stream);
 }
 
 template <int P>
 hipError_t launch_choose_t(const MlArgs& a, hipStream_t stream) {
-  auto* kernel = &choose_kernel<P>;
-  const size_t lds = choice_bytes(a.E, 1);
-  const hipError_t e = with_lds(kernel, lds);
-  if (e != hipSuccess) return e;
-  kernel<<<dim3(a.T), dim3(kMlThreads), lds, stream>>>(a);
-  return hipGetLastError();
+  return launch(&choose_kernel<P>, a.T, kMlThreads, choice_bytes(a.E, 1), stream, a);
 }
 
 hipError_t launch_choose(const MlArgs& a, hipStream_t stream) {
@@ -1018,42 +1018,28 @@ hipError_t launch_router(const MlArgs& a, hipStream_t stream) {
   // as few rounds as 1024 threads allow, and no more threads than they need
   const int pieces = a.H / 8, rounds = (pieces + kMlRouterThreads - 1) / kMlRouterThreads;
   const int threads = ((pieces + rounds - 1) / rounds + 63) / 64 * 64;
-  if (a.T == 1)
-    router_kernel<HALF, 1><<<dim3(a.E), dim3(threads), 0, stream>>>(a);
-  else if (a.T == 2)
-    router_kernel<HALF, 2><<<dim3(a.E), dim3(threads), 0, stream>>>(a);
-  else if (a.T <= 4)
-    router_kernel<HALF, 4><<<dim3(a.E), dim3(threads), 0, stream>>>(a);
-  else if (a.T <= 8)
-    router_kernel<HALF, 8><<<dim3(a.E), dim3(threads), 0, stream>>>(a);
-  else
-    router_kernel<HALF, 16><<<dim3(a.E), dim3(threads), 0, stream>>>(a);
-  return hipGetLastError();
+  if (a.T == 1) return launch(&router_kernel<HALF, 1>, a.E, threads, 0, stream, a);
+  if (a.T == 2) return launch(&router_kernel<HALF, 2>, a.E, threads, 0, stream, a);
+  if (a.T <= 4) return launch(&router_kernel<HALF, 4>, a.E, threads, 0, stream, a);
+  if (a.T <= 8) return launch(&router_kernel<HALF, 8>, a.E, threads, 0, stream, a);
+  return launch(&router_kernel<HALF, 16>, a.E, threads, 0, stream, a);
 }
 
 template <int GS, int KU>
 hipError_t launch_gate_up(const MlArgs& a, hipStream_t stream) {
   const size_t lds = gate_up_front(a.T, a.E) + ml_plan_bytes(a.most, a.E);
-  auto* kernel = &gate_up_kernel<GS, KU>;
-  const hipError_t e = with_lds(kernel, lds);
-  if (e != hipSuccess) return e;
   const long long tasks = static_cast<long long>(a.most) * (a.I / 16);
   const int grid = static_cast<int>(tasks < kModelCUs ? tasks : kModelCUs);
-  kernel<<<dim3(grid), dim3(kMlThreads), lds, stream>>>(a);
-  return hipGetLastError();
+  return launch(&gate_up_kernel<GS, KU>, grid, kMlThreads, lds, stream, a);
 }
 
 template <int GS, int NB, int AHEAD>
 hipError_t launch_down(const MlArgs& a, hipStream_t stream) {
   static_assert(NB <= kMlMaxNB, "room for the parts");
   const size_t lds = static_cast<size_t>(kMlWaves) * NB * 1024 + ml_plan_bytes(a.most, a.E);
-  auto* kernel = &down_kernel<GS, NB, AHEAD>;
-  const hipError_t e = with_lds(kernel, lds);
-  if (e != hipSuccess) return e;
   const int columns = (a.H / 16 + NB - 1) / NB;
   const int splits = columns < kModelCUs ? kModelCUs / columns : 1;
-  kernel<<<dim3(columns * splits), dim3(kMlThreads), lds, stream>>>(a, splits);
-  return hipGetLastError();
+  return launch(&down_kernel<GS, NB, AHEAD>, columns * splits, kMlThreads, lds, stream, a, splits);
 }
 
 template <int GS>
