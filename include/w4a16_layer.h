@@ -166,10 +166,10 @@ size_t w4a16_moe_layer_workspace_bytes(int T, int experts, int top_k, int hidden
  * Supported: 0 <= T <= W4A16_MOE_LAYER_MAX_TOKENS, group in {32, 64, 128, 256},
  * hidden % group == 0, width % group == 0, one expert's packed matrix and the
  * T * top_k inner rows below 4 GB (else W4A16_ERR_UNSUPPORTED; more tokens take
- * w4a16_moe_route and the calls behind it). x, router, the packed weights and scales, base and out 16-byte
- * aligned, workspace 256-byte, the rest 4-byte. T == 0 launches nothing. Three
- * launches on `stream` for up to 64 experts, or one or two tokens of up to 256,
- * else four. ids and weights are handed from one launch to the next.
+ * w4a16_moe_route and the calls behind it). x, router, the packed weights and
+ * scales, base and out 16-byte aligned, workspace 256-byte, the rest 4-byte.
+ * T == 0 launches nothing. Three or four launches on `stream`, which hand ids and
+ * weights from one to the next.
  * Returns W4A16_OK, W4A16_ERR_INVALID_ARG (null pointer, bad field, workspace
  * too small), W4A16_ERR_UNSUPPORTED, W4A16_ERR_MISALIGNED or W4A16_ERR_LAUNCH.
  */

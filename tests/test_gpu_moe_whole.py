@@ -150,6 +150,19 @@ def test_groups_of_experts(E, groups, kept, top, scoring, bias):
         w.check(6, k, scoring=scoring, groups=groups, groups_kept=kept, group_top=top, scale=1.25)
 
 
+@pytest.mark.parametrize("T,E", [(1, 4), (1, 65), (1, 132), (1, 256), (1, 260), (2, 64), (2, 128), (2, 132), (2, 256),
+                                 (8, 64), (9, 64), (16, 8)])
+def test_where_the_choice_is_made(T, E):
+    """Tokens and experts on both sides of where the choice gets a launch of its own,
+    by the logit and by values within groups."""
+    w = Whole(E, 64, 32, 32, 7 * E + T, bias=True)
+    w.check(T, min(E, 8), renormalize=False)
+    w.check(T, min(E, 8), scoring="sigmoid", pad=T // 4)
+    if E % 4 == 0:
+        w.check(T, min(E // 2, 32), groups=4, groups_kept=2, group_top=2, scale=2.5)
+    Whole(E, 64, 32, 32, 7 * E + T, half=True).check(T, min(E, 32))
+
+
 def test_equal_logits():
     """Experts with the same router row: the lowest index wins; with groups, the lowest
     group."""

@@ -215,8 +215,9 @@ __device__ __forceinline__ void merge_two(uint64_t& first, uint64_t& second, uin
   second = low > high ? low : high;
 }
 
-// One token's experts by the rule of w4a16_moe_route, in fp64 throughout; a wave does
-// all of it, or the part-th of several a share of the scores and of the comparisons. P: experts per lane, expert i * 64 + lane the i-th.
+// One token's experts by the rule of w4a16_moe_route, in fp64 throughout; a wave does all
+// of it, or as the part-th of several a share of the scores and of the comparisons. P:
+// experts per lane, expert i * 64 + lane the i-th.
 template <int P>
 struct Choice {
   const MlArgs& a;
@@ -422,9 +423,9 @@ __host__ __device__ constexpr size_t choice_bytes(int E, int shared_tokens) {
 
 // The experts of tokens t0 .. t0 + T - 1 (T = 1 or 2), the waves shared evenly, into
 // ids[i][kMlMaxK] and chosen of the i-th. Every thread. Places are counted where that is
-// less work than top_k rounds over the wave (128 experts on 8 waves 0.3 us, a round some
-// 0.2; 256 experts 0.9, a round 0.4). beside: loads of every wave that are wanted behind
-// the choice.
+// less work than top_k rounds over the wave (us of the whole layer, counted / by rounds, 8
+// per token: 1 token of 128 experts 28.9 / 29.3, of 256 20.8 / 21.7; 4 tokens of 512 36.8 /
+// 36.3). beside: loads of every wave that are wanted behind the choice.
 template <int P, typename F>
 __device__ __forceinline__ void choose_together(const MlArgs& a, int t0, int T, unsigned char* lds,
                                                 short (*ids)[kMlMaxK], float (*chosen)[kMlMaxK], bool write, F beside) {
@@ -451,29 +452,27 @@ __device__ __forceinline__ void choose_together(const MlArgs& a, int t0, int T, 
   if (wave % parts == 0) c.finish(c.order(count ? larger : nullptr), ids[i0], chosen[i0], write);
 }
 
-// All tokens' experts, up to 64 of them, a wave for a token.
+// The experts, up to 64, of up to kMlWaves tokens, a wave for a token.
 template <typename F>
 __device__ __forceinline__ void choose_each(const MlArgs& a, unsigned char* lds, short (*ids)[kMlMaxK],
                                             float (*chosen)[kMlMaxK], bool write, F beside) {
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  bool first = true;
-  for (int t = wave; t < a.T; t += kMlWaves, first = false) {
-    Choice<1> c(a, t, lane, 0, 1, reinterpret_cast<uint64_t*>(lds) + wave * 64, nullptr, [&] {
-      if (first) beside();
-    });
-    int larger[1];
-    c.count_larger(larger);
-    c.finish(c.order(larger), ids[t], chosen[t], write);
-  }
-  if (wave >= a.T) beside();
+  const int lane = threadIdx.x & 63, t = uniform(threadIdx.x >> 6);
+  if (t >= a.T) return beside();
+  Choice<1> c(a, t, lane, 0, 1, reinterpret_cast<uint64_t*>(lds) + t * 64, nullptr, beside);
+  int larger[1];
+  c.count_larger(larger);
+  c.finish(c.order(larger), ids[t], chosen[t], write);
 }
 
-// Whether every workgroup of gate_up_kernel makes the choice itself: for one or two
-// tokens, whose work 8 waves share, and for few experts. Otherwise a launch of its own, a
-// workgroup per token, is ahead (us of gate_up_kernel before its first weights, of both
-// launches with one: 4 tokens of 256 experts in groups 12.2 / 7.6, 16 of 128 12.9 / 7.1;
-// 1 of 128 4.5 / 6.7).
-__host__ __device__ constexpr bool choose_inside(int T, int E) { return E <= 64 || (T <= 2 && E <= 256); }
+// Whether every workgroup of gate_up_kernel makes the choice itself: up to 64 experts a
+// wave does a token, and up to two tokens the 8 waves share the work. Otherwise a launch
+// of its own, a workgroup per token, is ahead. us of the whole layer, inside / its own
+// launch, 8 experts per token: 128 experts of 5120 x 1024 at 1 token 28.9 / 29.8, at 16
+// 120 / 114; 256 of 2048 x 512 at 1 token 20.8 / 21.8, at 2 26.4 / 26.0; 128 at 2 23.8 /
+// 24.2; 64 at 1 18.5 / 19.7, at 8 33.3 / 33.4; 4 of 64 at 16 37.6 / 35.7.
+__host__ __device__ constexpr bool choose_inside(int T, int E) {
+  return E <= 64 ? T <= kMlWaves : T <= 2 && T * E <= 256;
+}
 
 template <int P>
 __global__ __launch_bounds__(kMlThreads) void choose_kernel(const MlArgs a) {
@@ -1007,6 +1006,7 @@ hipError_t launch_choose_t(const MlArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_choose(const MlArgs& a, hipStream_t stream) {
+  if (a.E <= 64) return launch_choose_t<1>(a, stream);
   if (a.E <= 128) return launch_choose_t<2>(a, stream);
   if (a.E <= 256) return launch_choose_t<4>(a, stream);
   if (a.E <= 512) return launch_choose_t<8>(a, stream);
