@@ -199,3 +199,29 @@ def test_far_rows():
     ref, tol = layer_ref.epilogue(x[at].double().cpu().numpy(), c.q, c.s, 128, "swiglu",
                                   residual=np.full((7, N // 2), 0.5))
     moe_ref.check(host_bits(y[at]), ref, tol)
+
+
+@pytest.mark.parametrize("M", [1, 16, 17, 32, 40])
+def test_gated_weights_past_4_gb(M):
+    """More weights than the tiles' 32-bit offsets reach, at the row counts whose form
+    comes in no pairs and beside them. Columns repeat every 1024, and the up half begins
+    in the middle of a repetition."""
+    import torch
+
+    import w4a16_weight_only_gemm_amd as w4
+    K, part, group = 1024, 1024, 128
+    N = (2 ** 33 // K // (2 * part) + 2) * 2 * part + part
+    assert w4.w4a16_qweight_bytes(N, K) > 2 ** 32 and (N // 2) % part == part // 2
+    c = Case(M, part, K, group, M)
+    times = N // part
+    qw, sp = c.qw.repeat(times), c.sp.repeat(times)
+    y = torch.full((M + 1, N // 2), -3.0, dtype=torch.bfloat16, device="cuda")
+    w4.w4a16_gemm_epilogue(c.dx, qw, sp, y[:M], M, N, K, group, act=w4.W4A16_ACT_SWIGLU)
+    assert bool((y[M] == -3.0).all())
+    up = (np.arange(part) + N // 2) % part
+    ref, tol = layer_ref.epilogue(moe_ref.bf16_value(c.x), np.concatenate([c.q, c.q[up]]),
+                                  np.concatenate([c.s, c.s[up]]), group, "swiglu")
+    first = y[:M, :part].contiguous()
+    moe_ref.check(host_bits(first), ref, tol, M)
+    for i in range(1, N // 2 // part):  # every repetition has the first's bits
+        assert torch.equal(y[:M, i * part:(i + 1) * part], first), i

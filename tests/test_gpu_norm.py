@@ -261,3 +261,27 @@ def test_far_rows():
         moe_ref.check(host_bits(r[at]), a, da + BF16 * (np.abs(a) + da))
         moe_ref.check(host_bits(x[at]), v, dv + BF16 * (np.abs(v) + dv))
         del r, x, y
+
+
+def test_codes_of_tiny_rows():
+    """Rows whose 127 / max is past fp32: codes still follow the values. A value is off by
+    a few half steps of fp32 and by half a step of the smallest number, 2^-150, which is
+    2^-150 * 127 / max < 2^-16 of a code here."""
+    import torch
+
+    import w4a16_weight_only_gemm_amd as w4
+    rng = np.random.default_rng(5)
+    T, N = 3, 64
+    y = moe_ref.bf16_bits(rng.standard_normal((T, N)).astype(np.float32))
+    w = np.full(N, 2.0 ** -126, np.float32)
+    xq = torch.full((T, N), 99, dtype=torch.int8, device="cuda")
+    sx = torch.full((T,), -3.0, dtype=torch.float32, device="cuda")
+    w4.w4a16_norm(T, N, y=dev_bf16(y), weight=dev_bf16(moe_ref.bf16_bits(w)), xq=xq, sx=sx)
+    torch.cuda.synchronize()
+    yv = moe_ref.bf16_value(y)
+    v = yv / np.sqrt((yv * yv).mean(1, keepdims=True) + float(np.float32(1e-6))) * 2.0 ** -126
+    a = np.abs(v).max(1, keepdims=True)
+    assert np.all(a < 127.0 / 2.0 ** 128)
+    q = layer_ref.natural(xq.cpu().numpy()).astype(np.float64)
+    assert np.all(np.abs(q - v * 127.0 / a) <= 0.5 + 2.0 ** -10)
+    assert np.all(np.abs(sx.double().cpu().numpy() - a[:, 0] / 127.0) <= 2.0 ** -148)

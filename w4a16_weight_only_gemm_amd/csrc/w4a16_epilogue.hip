@@ -163,7 +163,7 @@ int gated_form(int M, int N, int K, int group) {
     case kOne16: return kTwo16;
     case kXs1x3w4: case kXs1x5w4: return N / 32 / 3 >= kModelCUs ? kXs1x6w4 : kXs1x2w4;
     case kXs1x5: return kXs1x4;
-    case kXs2x3: case kXs2x5: return kXs2x4;
+    case kXs2x3: case kXs2x5: case kXs2x5w4: return kXs2x4;
     default: return f;
   }
 }
@@ -172,7 +172,7 @@ template <int GS>
 hipError_t launch_epilogue_g(const GemmArgs& a, const Epilogue& ep, bool gated, hipStream_t stream) {
   if constexpr (GS <= 128) {
     // The 4-wave form of 2 x 5 blocks has no twin in pairs as good as the tiles (2 x 4 blocks
-    // at 24 rows, 5120 x 34816: 36.2 us, tiles 32.1).
+    // at 24 rows, 5120 x 34816: 36.2 us, tiles 32.1), which end at weights of 4 GB.
     const bool tiles = choose_path(a.M, a.N, a.K, GS) == W4A16_PATH_LARGE ||
                        (gated && a.M <= kPlainMaxRows && plain_form(a.M, a.N, a.K, GS) == kXs2x5w4);
     if (tiles && large_runs(a.N, a.K, GS)) {

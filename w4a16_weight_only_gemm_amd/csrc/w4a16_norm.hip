@@ -255,14 +255,16 @@ __global__ __launch_bounds__(BLOCK ? 64 * kNormMaxWaves : 256) void norm_kernel(
                     to_bf16(v[p]), span[p].left);
     return;
   }
-  // The codes and scale of w4a8_quantize, of values that were not rounded before.
+  // The codes and scale of w4a8_quantize, of values that were not rounded before. 127 /
+  // max is past fp32 for a row below 2^-121, which is raised by a power of two first.
   float big = 0.f;
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
     for (int j = 0; j < 8; ++j) big = fmaxf(big, fabsf(v[p].v[j]));
   big = join(big, [](float x, float y) { return fmaxf(x, y); });
-  const float inv = big > 0.f ? 127.f / big : 0.f;
+  const float raise = big < 0x1p-100f ? 0x1p64f : 1.f;
+  const float inv = big > 0.f ? 127.f / (big * raise) : 0.f;
   if (mine == 0) to_global(a.sx)[row] = big / 127.f;
 #pragma unroll
   for (int p = 0; p < P; ++p) {
@@ -270,7 +272,7 @@ __global__ __launch_bounds__(BLOCK ? 64 * kNormMaxWaves : 256) void norm_kernel(
     uint32_t c[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float q = __builtin_rintf(v[p].v[j] * inv);
+      float q = __builtin_rintf(v[p].v[j] * raise * inv);
       q = q > 127.f ? 127.f : q;
       q = q < -127.f ? -127.f : q;
       c[j] = static_cast<uint32_t>(static_cast<int>(q)) & 0xFFu;
