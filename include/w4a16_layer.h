@@ -152,7 +152,7 @@ size_t w4a16_moe_layer_workspace_bytes(int T, int experts, int top_k, int hidden
  *   ids, weights: the choice that w4a16_moe_route defines, from these logits;
  *     a token whose `live` is 0 is routed nowhere (ids -1, weights 0)
  *   h[t][j] = silu(x[t] . gate half) * (x[t] . up half) of expert ids[t][j],
- *     rounded to bf16
+ *     held to 16 bits (two bf16)
  *   out[t] = base[t] + sum_j weights[t][j] * (h[t][j] . down of expert ids[t][j])
  * with fp32 products and sums and one rounding to bf16 at the end. A result
  * does not depend on timing: the same call gives the same bits.
@@ -164,8 +164,8 @@ size_t w4a16_moe_layer_workspace_bytes(int T, int experts, int top_k, int hidden
  *   ids  : device int32 [T][top_k]; weights : device f32 [T][top_k]
  *   workspace : w4a16_moe_layer_workspace_bytes(...) bytes
  * Supported: 0 <= T <= W4A16_MOE_LAYER_MAX_TOKENS, group in {32, 64, 128, 256},
- * hidden % group == 0, width % group == 0, one expert's packed matrix and the
- * T * top_k inner rows below 4 GB (else W4A16_ERR_UNSUPPORTED; more tokens take
+ * hidden % group == 0, width % group == 0, one expert's packed matrix and
+ * 4 * T * top_k * width bytes below 4 GB (else W4A16_ERR_UNSUPPORTED; more tokens take
  * w4a16_moe_route and the calls behind it). x, router, the packed weights and
  * scales, base and out 16-byte aligned, workspace 256-byte, the rest 4-byte.
  * T == 0 launches nothing. Three or four launches on `stream`, which hand ids and

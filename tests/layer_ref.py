@@ -140,10 +140,11 @@ def natural(c: np.ndarray) -> np.ndarray:
 def moe_layer(x, logits, q_up, s_up, q_down, s_down, group, top_k, base=None, live=None,
               bias=None, **route):
     """x fp64 [T][H], logits fp64 [T][E] (their definition is the caller's), experts' codes
-    and scales. Returns ids, weights, out, bound. h is off by its product's bound and its
-    bf16 rounding (moe_ref.experts); down's biased sums run over the groups of all chosen
-    experts, waves and parts: group + top_k G + 40 half steps of their weighted
-    magnitudes, and the weights' own rounding."""
+    and scales. Returns ids, weights, out, bound. h is off by its product's bound (that
+    of moe_ref.experts without its last rounding) and held as two bf16: the second rounds
+    a remainder of at most 2^-8 of it by 2^-8. down's biased sums run over both, and over
+    the groups of all chosen experts, waves and parts: 2 group + top_k G + 44 half steps
+    of their weighted magnitudes, and the weights' own rounding."""
     z = np.array(logits, np.float64)
     if live is not None:
         z[np.asarray(live) == 0] = -np.inf
@@ -151,6 +152,8 @@ def moe_layer(x, logits, q_up, s_up, q_down, s_down, group, top_k, base=None, li
     T, E = z.shape
     H, I = q_down.shape[1:]
     h, dh = moe_ref.experts(x, q_up, s_up, rows, off, top_k, group, True)
+    dh = (dh - BF16 * np.abs(h)) / (1 + BF16)
+    dh = dh + BF16 ** 2 * (np.abs(h) + dh)
     out = np.zeros((T, H)) if base is None else base.copy()
     d = np.zeros((T, H))
     for t in range(T):
@@ -162,8 +165,8 @@ def moe_layer(x, logits, q_up, s_up, q_down, s_down, group, top_k, base=None, li
             se = np.repeat(s_down[e], group, axis=1)
             wd = q_down[e] * se
             out[t] += w[t, j] * (wd @ h[sl])
-            mag = ((np.abs(24.0 + q_down[e]) + 24.0) * np.abs(se)) @ (np.abs(h[sl]) + dh[sl])
+            mag = ((np.abs(24.0 + q_down[e]) + 24.0) * np.abs(se)) @ ((1 + 2 * BF16) * np.abs(h[sl]) + dh[sl])
             d[t] += abs(w[t, j]) * (np.abs(wd) @ dh[sl]
-                                    + (group + top_k * (I // group) + 40) * F32 * mag)
+                                    + (2 * group + top_k * (I // group) + 44) * F32 * mag)
     d = d + F32 * (np.abs(out) + d)
     return ids, w, out, d + BF16 * (np.abs(out) + d)

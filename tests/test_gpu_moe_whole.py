@@ -110,8 +110,8 @@ class Whole:
         assert np.all(np.abs(gw - w) <= moe_ref.F32 * np.abs(w) + 1e-12 * (1 + np.abs(w)))
         gv = moe_ref.bf16_value(got[:T])
         assert np.all(np.abs(gv - out) <= tol), float(np.max(np.abs(gv - out) - tol))
-        # bf16 roundings of h and out
-        assert np.linalg.norm(gv - out) <= 2 * moe_ref.BF16 * max(np.linalg.norm(out), 1e-30)
+        # the rounding of out, and of nothing else to bf16
+        assert np.linalg.norm(gv - out) <= moe_ref.BF16 * max(np.linalg.norm(out), 1e-30)
 
 
 @pytest.mark.parametrize("group", [32, 64, 128, 256])

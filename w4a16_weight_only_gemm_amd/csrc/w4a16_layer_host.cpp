@@ -102,7 +102,7 @@ int w4a16_moe_layer(const w4a16_moe_layer_args* l, const void* x, const int32_t*
   if (H < 1 || I < 1 || !group_supported(group) || H % group != 0 || I % group != 0) return W4A16_ERR_UNSUPPORTED;
   // the matrices, and the inner rows, are read through 32-bit offsets
   if (I > 0x3FFFFFFF || w4a16_qweight_bytes(2 * I, H) > kMaxMatrix ||
-      static_cast<size_t>(T) * c.top_k * I * 2 > kMaxMatrix)
+      static_cast<size_t>(T) * c.top_k * I * 4 > kMaxMatrix)
     return W4A16_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < w4a16_moe_layer_workspace_bytes(T, c.experts, c.top_k, H, I))
     return W4A16_ERR_INVALID_ARG;

@@ -16,13 +16,14 @@
 //    range in registers, while the weights of one (expert, 16 gate and 16 up columns)
 //    after the other stream by, a whole task ahead. The waves' sums meet in LDS, where
 //    SwiGLU is formed. 16 tokens of 128 experts, 5120 x 1024: 6.7 TB/s while it streams.
+//    SwiGLU's values are stored as two bf16 (down_kernel says why).
 //  * down_kernel: the active experts' k ranges laid end to end are one long sum for every
 //    16 columns of the output, each expert's part weighted by its tokens' weights on the
 //    way. A workgroup takes a few column blocks of an even part of it; the parts are
 //    added by the last workgroup to finish one, in their order, so results do not depend
 //    on timing.
-// Bound by HBM from a few tokens on (16 tokens: 113 us, 82 of them streaming); at one
-// token (27 us) by three launches' ramps and by the chain logits, choice, first
+// Bound by HBM from a few tokens on (16 tokens: 118 us, 85 of them streaming); at one
+// token (28 us) by three launches' ramps and by the chain logits, choice, first
 // weights. Gate, up and down in one launch, whose workgroups wait for the inner rows with
 // down's first weights on their way, took 30 us there and 123 at 16 tokens: the rows'
 // way through memory and the polls behind the weights cost more than a launch.
@@ -60,7 +61,7 @@ MlSpace ml_space(int T, int E, int top_k, int H, int I) {
   // the counters are in front
   s.logits = up256((static_cast<size_t>(H) + 15) / 16 * 4);
   s.h = s.logits + up256(static_cast<size_t>(T) * E * 8);
-  s.parts = s.h + up256(static_cast<size_t>(T) * top_k * I * 2);
+  s.parts = s.h + up256(static_cast<size_t>(T) * top_k * I * 4);
   // 16 x 16 floats for every column block of every split: at most kModelCUs splits
   // of kMlMaxNB blocks (one split needs none)
   s.total = s.parts + static_cast<size_t>(kModelCUs) * kMlMaxNB * kMlPartFloats * 4;
@@ -81,7 +82,7 @@ struct MlArgs {
   int* ids;
   float* weights;
   double* logits;   // [T][E]
-  uint16_t* h;      // bf16 [T][top_k][I]
+  uint16_t* h;      // bf16 [T][top_k][I / 8][2][8]: values, what their rounding left
   float* parts;     // [columns][splits][blocks][16][16]
   int* counters;    // [H / 16]: parts that are there of every group of columns
   int T, E, top_k, H, I;
@@ -793,7 +794,11 @@ __global__ __launch_bounds__(kMlThreads) void gate_up_kernel(const MlArgs a) {
           up += mine[((w * 2 + 1) * 4 + (tid >> 6)) * 64 + lane];
         }
         const size_t slot = static_cast<size_t>(t) * a.top_k + tb.place[at * 16 + t];
-        to_global(a.h)[slot * a.I + c * 16 + c16] = f32_to_bf16_bits(silu(gate) * up);
+        const float v = silu(gate) * up;
+        const uint16_t hi = f32_to_bf16_bits(v);
+        const gptr<uint16_t> h = to_global(a.h) + slot * (2 * static_cast<size_t>(a.I)) + c * 32 + (c16 & 8) * 2 + (c16 & 7);
+        h[0] = hi;
+        h[8] = f32_to_bf16_bits(v - bf16_bits_to_f32(hi));
       }
     }
     turn ^= 1;
@@ -805,7 +810,14 @@ __global__ __launch_bounds__(kMlThreads) void gate_up_kernel(const MlArgs a) {
 // of them a wave has on the way. 4 and 2: 4 blocks, 3 and 4 units and 5 blocks, 2 units
 // took up to 1.5 us more at 1, 3, 4 and 16 tokens. For one token of 8 experts, inner rows
 // through LDS, 2 blocks and all of a wave's 8 units on the way without splits: the same.
-template <int GS, int NB, int AHEAD>
+// Inner rows are two bf16 each, the value and what its rounding left (16 bits in all):
+// rounded to one, their error would be as large as the output's own rounding. PAIR, up to
+// 8 tokens: the second of token t is row t + 8 of the same matrix instructions, and the
+// rows' sums are added at the end. More tokens take a second instruction on the same
+// weights. us of the whole layer with one bf16, two in pairs, two in two instructions: 1
+// token of 128 experts, 5120 x 1024, 28.5 / 28.8 / 30.3, 4 of 256 45.3 / 45.6 / 47.1, 16 of
+// 128 113 / - / 118 (pairs wherever an expert's tokens allow it: 118).
+template <int GS, int NB, int AHEAD, bool PAIR>
 __global__ __launch_bounds__(kMlThreads) void down_kernel(const MlArgs a, int most_splits) {
   using U = MlUnit<GS>;
   extern __shared__ __attribute__((aligned(16))) unsigned char ml_lds[];
@@ -828,7 +840,7 @@ __global__ __launch_bounds__(kMlThreads) void down_kernel(const MlArgs a, int mo
       chosen = to_global(a.weights)[t * a.top_k + j];
     }
   }
-  const uint32_t h_bytes = static_cast<uint32_t>(a.T * a.top_k) * a.I * 2;
+  const uint32_t h_bytes = static_cast<uint32_t>(a.T * a.top_k) * a.I * 4;
   const __amdgpu_buffer_rsrc_t rh = make_rsrc(a.h, h_bytes);
   // Value i of the tile: block i / 256, row 4 (lane / 16) + i / 64 % 4 and column lane %
   // 16 of it, lane = i % 64. Whether there is such a value, and what is added to it.
@@ -858,7 +870,7 @@ __global__ __launch_bounds__(kMlThreads) void down_kernel(const MlArgs a, int mo
   const uint32_t scales = static_cast<uint32_t>(blocks) * groups * 16;
   struct Stage {
     MlWeights<GS> w[NB];
-    MlRows<GS> h;
+    MlRows<GS> h, l;
     int at, u;  // entry and unit of the expert
   };
   Stage ds[AHEAD];
@@ -892,15 +904,19 @@ __global__ __launch_bounds__(kMlThreads) void down_kernel(const MlArgs a, int mo
   auto load_inner = [&](Stage& s) {
     // other tokens' rows lie past the buffer and read as zeros, as do groups past
     // the last (its end is one of them)
-    const bool mine = s.at >= 0 && tb.mask[s.at] >> c16 & 1;
-    const uint32_t slot = mine ? c16 * a.top_k + tb.place[s.at * 16 + c16] : 0;
+    const int t = PAIR ? c16 & 7 : c16;
+    const bool mine = s.at >= 0 && tb.mask[s.at] >> t & 1;
+    const uint32_t slot = mine ? t * a.top_k + tb.place[s.at * 16 + t] : 0;
+    const uint32_t second = PAIR ? (c16 & 8) * 2 : 0;
 #pragma unroll
     for (int g = 0; g < U::G; ++g) {
       const int grp = s.u * U::G + g;
-      const uint32_t at = mine && grp < groups ? (slot * a.I + grp * GS + lg * U::WPL * 8) * 2 : 0xFFFFFE00u;
+      const uint32_t at = mine && grp < groups ? (slot * a.I + grp * GS + lg * U::WPL * 8) * 4 + second : 0xFFFFFE00u;
 #pragma unroll
-      for (int w = 0; w < U::WPL; ++w)
-        s.h.d[g * U::WPL + w] = __builtin_amdgcn_raw_buffer_load_b128(rh, at, 16 * w, 0);
+      for (int w = 0; w < U::WPL; ++w) {
+        s.h.d[g * U::WPL + w] = __builtin_amdgcn_raw_buffer_load_b128(rh, at, 32 * w, 0);
+        if constexpr (!PAIR) s.l.d[g * U::WPL + w] = __builtin_amdgcn_raw_buffer_load_b128(rh, at, 32 * w + 16, 0);
+      }
     }
   };
 #pragma unroll
@@ -911,20 +927,27 @@ __global__ __launch_bounds__(kMlThreads) void down_kernel(const MlArgs a, int mo
 #pragma unroll
   for (int b = 0; b < NB; ++b) y[b] = f32x4{0.f, 0.f, 0.f, 0.f};
   auto unit = [&](const Stage& s) {
-    const f32x4 wt = *reinterpret_cast<const f32x4*>(tb.weight + s.at * 16 + 4 * lg);
-    const int live = static_cast<uint16_t>(tb.mask[s.at]) >> (4 * lg);
+    const int t0 = 4 * (PAIR ? lg & 1 : lg);  // the token of the lane's first row
+    const f32x4 wt = *reinterpret_cast<const f32x4*>(tb.weight + s.at * 16 + t0);
+    const int live = static_cast<uint16_t>(tb.mask[s.at]) >> t0;
 #pragma unroll
     for (int g = 0; g < U::G; ++g) {
       if (U::G > 1 && s.u * U::G + g >= groups) break;  // uniform: K ends inside the unit
       f32x4 accb = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < U::WPL; ++w) accb = mfma16(act_frag(s.h.d[g * U::WPL + w]), bias, accb);
+      for (int w = 0; w < U::WPL; ++w) {
+        accb = mfma16(act_frag(s.h.d[g * U::WPL + w]), bias, accb);
+        if constexpr (!PAIR) accb = mfma16(act_frag(s.l.d[g * U::WPL + w]), bias, accb);
+      }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         f32x4 acc = accb;
 #pragma unroll
-        for (int w = 0; w < U::WPL; ++w)
-          acc = mfma16(act_frag(s.h.d[g * U::WPL + w]), dequant_biased(s.w[b].w[g * U::WPL + w]), acc);
+        for (int w = 0; w < U::WPL; ++w) {
+          const bf16x8 q = dequant_biased(s.w[b].w[g * U::WPL + w]);
+          acc = mfma16(act_frag(s.h.d[g * U::WPL + w]), q, acc);
+          if constexpr (!PAIR) acc = mfma16(act_frag(s.l.d[g * U::WPL + w]), q, acc);
+        }
         const float sc = scale_of(s.w[b].s[g], lane);
         // a row that is not the expert's takes nothing from it, whatever its values
 #pragma unroll
@@ -942,6 +965,12 @@ __global__ __launch_bounds__(kMlThreads) void down_kernel(const MlArgs a, int mo
     }
   }
 
+  if constexpr (PAIR) {  // rows t and t + 8 are 32 lanes apart
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) y[b][r] += __shfl_xor(y[b][r], 32);
+  }
   // the waves' sums, in wave order
 #pragma unroll
   for (int b = 0; b < NB; ++b)
@@ -1033,13 +1062,13 @@ hipError_t launch_gate_up(const MlArgs& a, hipStream_t stream) {
   return launch(&gate_up_kernel<GS, KU>, grid, kMlThreads, lds, stream, a);
 }
 
-template <int GS, int NB, int AHEAD>
+template <int GS, int NB, int AHEAD, bool PAIR>
 hipError_t launch_down(const MlArgs& a, hipStream_t stream) {
   static_assert(NB <= kMlMaxNB, "room for the parts");
   const size_t lds = static_cast<size_t>(kMlWaves) * NB * 1024 + ml_plan_bytes(a.most, a.E);
   const int columns = (a.H / 16 + NB - 1) / NB;
   const int splits = columns < kModelCUs ? kModelCUs / columns : 1;
-  return launch(&down_kernel<GS, NB, AHEAD>, columns * splits, kMlThreads, lds, stream, a, splits);
+  return launch(&down_kernel<GS, NB, AHEAD, PAIR>, columns * splits, kMlThreads, lds, stream, a, splits);
 }
 
 template <int GS>
@@ -1066,7 +1095,8 @@ hipError_t launch_moe_layer_g(const MlArgs& a, bool half, hipStream_t stream) {
   else
     e = launch_gate_up<GS, 0>(a, stream);
   if (e != hipSuccess) return e;
-  return launch_down<GS, 4, U::F == 4 ? 2 : 1>(a, stream);
+  constexpr int kAhead = U::F == 4 ? 2 : 1;
+  return a.T <= 8 ? launch_down<GS, 4, kAhead, true>(a, stream) : launch_down<GS, 4, kAhead, false>(a, stream);
 }
 
 }  // namespace
