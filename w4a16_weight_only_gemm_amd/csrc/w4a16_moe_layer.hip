@@ -22,11 +22,12 @@
 //    way. A workgroup takes a few column blocks of an even part of it; the parts are
 //    added by the last workgroup to finish one, in their order, so results do not depend
 //    on timing.
-// Bound by HBM from a few tokens on (16 tokens: 118 us, 85 of them streaming); at one
-// token (28 us) by three launches' ramps and by the chain logits, choice, first
-// weights. Gate, up and down in one launch, whose workgroups wait for the inner rows with
-// down's first weights on their way, took 30 us there and 123 at 16 tokens: the rows'
-// way through memory and the polls behind the weights cost more than a launch.
+// Bound by HBM from a few tokens on (16 tokens of 128 experts, 5120 x 1024: 118 to 127 us,
+// 4.7 to 5.0 TB/s over all of it); at one token (28 us) by three launches' ramps and by the
+// chain logits, choice, first weights. Gate, up and down in one launch, whose workgroups
+// wait for the inner rows with down's first weights on their way, took 30 us there and 123
+// at 16 tokens, when separate launches took 27 and 122: the rows' way through memory and
+// the polls behind the weights cost more than a launch.
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
