@@ -1,0 +1,15 @@
+// w4a16_sizes.h -- sizes that kernels form in 32 bits, without HIP, so that a host
+// test can hold them to 64-bit arithmetic.
+#pragma once
+
+#include <cstdint>
+
+namespace w4a16_internal {
+
+// Bytes of a packed matrix of `blocks` column blocks (16 columns of K codes, half a
+// byte each), below 4 GB. Halved before it is multiplied: N x K is past 2^32 from 2 GiB on.
+constexpr uint32_t packed_matrix_bytes(int blocks, int K) {
+  return static_cast<uint32_t>(blocks) * 8u * static_cast<uint32_t>(K);
+}
+
+}  // namespace w4a16_internal

@@ -11,6 +11,7 @@
 #include <cstdint>
 
 #include "w4a16_device.h"
+#include "w4a16_sizes.h"
 
 namespace w4a16_internal {
 
@@ -106,7 +107,7 @@ struct TileEngine {
     nt = nt_;
     xbytes = static_cast<uint32_t>(M - m0) * static_cast<uint32_t>(K) * 2u;
     xrow0 = x + static_cast<size_t>(m0) * K;
-    rq = make_rsrc(qw, static_cast<uint32_t>(NCB) * 16u * static_cast<uint32_t>(K) / 2u);
+    rq = make_rsrc(qw, packed_matrix_bytes(NCB, K));
     rs = make_rsrc(sp, static_cast<uint32_t>(NCB) * 16u * static_cast<uint32_t>(G) * 2u);
 #pragma unroll
     for (int nb = 0; nb < kLgNB; ++nb) {
@@ -133,7 +134,7 @@ struct TileEngine {
     NCB = (N + 15) / 16;
     xbytes = xbytes_;
     xrow0 = x;
-    rq = make_rsrc(qw, static_cast<uint32_t>(NCB) * 16u * static_cast<uint32_t>(K) / 2u);
+    rq = make_rsrc(qw, packed_matrix_bytes(NCB, K));
     rs = make_rsrc(sp, static_cast<uint32_t>(NCB) * 16u * static_cast<uint32_t>(G) * 2u);
     blk[0] = blk0 < NCB ? blk0 : NCB - 1;
     blk[1] = blk1 < NCB ? blk1 : NCB - 1;

@@ -43,6 +43,7 @@
 #include <cstdint>
 
 #include "w4a16_device.h"
+#include "w4a16_sizes.h"
 #include "w4a8_launch.h"
 
 namespace w4a16_internal {
@@ -223,7 +224,7 @@ struct Q8Engine {
     nt = nt_;
     xbytes = static_cast<uint32_t>(M - m0) * static_cast<uint32_t>(K);
     xrow0 = a.xq + static_cast<size_t>(m0) * K;
-    rq = make_rsrc(a.qweight, static_cast<uint32_t>(NCB) * 16u * static_cast<uint32_t>(K) / 2u);
+    rq = make_rsrc(a.qweight, packed_matrix_bytes(NCB, K));
     rs = make_rsrc(a.scales, static_cast<uint32_t>(NCB) * 16u * static_cast<uint32_t>(G) * 2u);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
