@@ -39,6 +39,7 @@
 #include "w4a16_lanes.h"
 #include "w4a16_launch.h"
 #include "w4a16_layer_launch.h"
+#include "w4a16_sizes.h"
 
 namespace w4a16_internal {
 namespace {
@@ -584,17 +585,17 @@ __device__ __forceinline__ MlMatrix matrix_at(const uint32_t* w, const uint16_t*
           make_rsrc(s + static_cast<size_t>(expert) * scales, scales * 2u), there};
 }
 
-// Unit u of a column block whose first tile is `tile` (block * groups); groups past the
-// last are others' and not used.
+// Unit u of a column block whose first tile is `tile` (block * groups); of groups past the
+// last the last is read again and not used.
 template <int GS>
-__device__ __forceinline__ void load_unit(MlWeights<GS>& r, const MlMatrix& m, int tile, int u, int lane) {
+__device__ __forceinline__ void load_unit(MlWeights<GS>& r, const MlMatrix& m, int tile, int u, int groups, int lane) {
   using U = MlUnit<GS>;
   constexpr int kOnce = 2;  // the instruction's nt bit
   const uint32_t far = 0xFFFFFE00u;
   const uint32_t wl = m.there ? lane * U::WPL * 4 : far, sl = m.there ? (lane & 14) * 2 : far;
 #pragma unroll
   for (int g = 0; g < U::G; ++g) {
-    const uint32_t at = tile + u * U::G + g;
+    const uint32_t at = tile + (U::G > 1 ? unit_group(u, U::G, g, groups) : u);
     const int wat = static_cast<int>(at * (256u * U::WPL));
     if constexpr (U::WPL >= 4) {
 #pragma unroll
@@ -626,7 +627,7 @@ __device__ __forceinline__ void load_rows(MlRows<GS>& r, gptr<const uint16_t> ro
   const int lg = (threadIdx.x & 63) >> 4;
 #pragma unroll
   for (int g = 0; g < U::G; ++g) {
-    const int grp = min(u * U::G + g, groups - 1);
+    const int grp = unit_group(u, U::G, g, groups);
 #pragma unroll
     for (int w = 0; w < U::WPL; ++w)
       r.d[g * U::WPL + w] =
@@ -727,7 +728,7 @@ __global__ __launch_bounds__(kMlThreads) void gate_up_kernel(const MlArgs a) {
     m.there = m.there && k < n;
     const int u = min(u0 + k, up_units - 1);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) load_unit<GS>(st[slot][q], m, p.tile + q * up_tiles, u, lane);
+    for (int q = 0; q < 2; ++q) load_unit<GS>(st[slot][q], m, p.tile + q * up_tiles, u, up_groups, lane);
     if constexpr (KU == 0) load_rows<GS>(xs[slot], row, u, up_groups);
   };
   constexpr int kTaskFloats = kMlWaves * 2 * 256;  // red: [2][waves][2][4][64]
@@ -891,7 +892,7 @@ __global__ __launch_bounds__(kMlThreads) void down_kernel(const MlArgs a, int mo
     for (int b = 0; b < NB; ++b) {
       MlMatrix mb = m;
       mb.there = there && b0 + b < blocks;
-      load_unit<GS>(s.w[b], mb, min(b0 + b, blocks - 1) * groups, s.u, lane);
+      load_unit<GS>(s.w[b], mb, min(b0 + b, blocks - 1) * groups, s.u, groups, lane);
     }
     next_at += at_step;
     next_u += u_step;

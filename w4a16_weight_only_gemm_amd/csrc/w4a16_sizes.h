@@ -12,4 +12,11 @@ constexpr uint32_t packed_matrix_bytes(int blocks, int K) {
   return static_cast<uint32_t>(blocks) * 8u * static_cast<uint32_t>(K);
 }
 
+// The g-th group of a wave's unit u of `per` groups, the last one again where K ends inside
+// the unit: what a scalar offset past the end of a buffer reads is not the range check's to
+// decide.
+constexpr int unit_group(int u, int per, int g, int groups) {
+  return u * per + g < groups ? u * per + g : groups - 1;
+}
+
 }  // namespace w4a16_internal
