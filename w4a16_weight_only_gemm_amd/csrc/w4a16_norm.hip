@@ -5,9 +5,10 @@
 //
 // Every row is read once into registers, eight columns to a 16-byte piece, and
 // stays there in fp32 through both norms; the means are taken of the registers (of
-// the deviations from the mean, in a second pass over them, for layer norms), and
-// r and v are rounded once, on their way out. A row belongs to 16, 32 or 64 lanes
-// of a wave (DPP sums, no LDS) or to the waves of a workgroup (one barrier a sum).
+// the deviations from the mean, in a second pass over them, for layer norms; after
+// two more where the mean's rounding counts among them), and r and v are rounded
+// once, on their way out. A row belongs to 16, 32 or 64 lanes of a wave (DPP sums, no
+// LDS) or to the waves of a workgroup (one barrier a sum).
 // What bounds it: HBM for many rows; for few, the launch and the chain of a load,
 // the sums and a store.
 #include <hip/hip_runtime.h>
@@ -161,7 +162,7 @@ __global__ __launch_bounds__(BLOCK ? 64 * kNormMaxWaves : 256) void norm_kernel(
   const long long row = BLOCK ? static_cast<long long>(blockIdx.x)
                               : static_cast<long long>(blockIdx.x) * (256 / L) + threadIdx.x / L;
   if (!BLOCK && row >= args.T) return;  // whole rows of lanes; no barrier follows
-  const float n = static_cast<float>(N);  // sums are divided: a constant row's mean is its value
+  const float n = static_cast<float>(N);
   const bool layer = a.kind == W4A16_NORM_LAYER;
   const float one = a.unit_offset ? 1.f : 0.f;
   const bool wide = a.residual_type == W4A16_RESIDUAL_F32;
@@ -184,26 +185,53 @@ __global__ __launch_bounds__(BLOCK ? 64 * kNormMaxWaves : 256) void norm_kernel(
   Piece v[P];
   // (v - mean) / sqrt(mean square + eps) * weight + bias, in place; columns past N
   // hold zeros and stay out of the sums
-  auto normalise = [&](const void* w, const void* b) {
-    if (layer) {
-      float s = 0.f;
+  auto mean_of = [&] {
+    float s = 0.f;
 #pragma unroll
-      for (int p = 0; p < P; ++p)
+    for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s += v[p].v[j];
-      const float mean = sum(s) / n;
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          v[p].v[j] = (TAIL ? j < span[p].left : span[p].left > 0) ? v[p].v[j] - mean : 0.f;
-    }
+      for (int j = 0; j < 8; ++j) s += v[p].v[j];
+    return sum(s) / n;
+  };
+  auto mean_square = [&] {
     float s = 0.f;
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
       for (int j = 0; j < 8; ++j) s = __builtin_fmaf(v[p].v[j], v[p].v[j], s);
-    const float r = 1.f / sqrtf(sum(s) / n + a.eps);
+    return sum(s) / n;
+  };
+  auto subtract = [&](float m) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      int left = span[p].left;
+      // compared here: masks of all columns, made once for every use, fill the registers
+      asm volatile("" : "+v"(left));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[p].v[j] = (TAIL ? j < left : left > 0) ? v[p].v[j] - m : 0.f;
+    }
+  };
+  auto normalise = [&](const void* w, const void* b) {
+    float mean = 0.f;
+    if (layer) {
+      mean = mean_of();
+      subtract(mean);
+    }
+    float square = mean_square();
+    // The sum of a row rounds by up to some 90 half steps of its mean, which count among
+    // deviations that are small against it: beyond 64 times their root mean square (a
+    // condition of the row, the same in all its threads) they are taken from the fp32
+    // number next to the mean, which is the value itself in a row of equal ones, and then
+    // from their own mean. A loop, so that it takes no registers from the usual way.
+    if (mean * mean * 0x1p-12f > square) {
+#pragma unroll 1
+      for (int round = 0; round < 2; ++round) {
+        const float m = mean_of();
+        subtract(round == 0 ? (mean + m) - mean : m);
+      }
+      square = mean_square();
+    }
+    const float r = 1.f / sqrtf(square + a.eps);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const Piece wp = bf16_piece(w ? bf16_row(w, 0, p) : none), bp = bf16_piece(b ? bf16_row(b, 0, p) : none);
@@ -295,13 +323,14 @@ __global__ __launch_bounds__(64) void norm_short_kernel(const NormArgs args) {
   auto bf16_at = [](const void* p, long long i) { return bf16_bits_to_f32(to_global(static_cast<const uint16_t*>(p))[i]); };
   float v[7];
   auto normalise = [&](const void* w, const void* b) {
-    float mean = 0.f, s = 0.f;
+    double mean = 0.0;  // of at most 7 values: exact but for the quotient
+    float s = 0.f;
     if (a.kind == W4A16_NORM_LAYER) {
       for (int j = 0; j < 7; ++j) mean += j < N ? v[j] : 0.f;
       mean /= n;
     }
     for (int j = 0; j < 7; ++j) {
-      v[j] -= mean;
+      v[j] = static_cast<float>(v[j] - mean);
       s += j < N ? v[j] * v[j] : 0.f;
     }
     const float r = 1.f / sqrtf(s / n + a.eps);
