@@ -13,6 +13,7 @@
 // the sums and a store.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cstdint>
 
 #include "w4a16_device.h"
@@ -193,12 +194,15 @@ __global__ __launch_bounds__(BLOCK ? 64 * kNormMaxWaves : 256) void norm_kernel(
       for (int j = 0; j < 8; ++j) s += v[p].v[j];
     return sum(s) / n;
   };
-  auto mean_square = [&] {
+  auto mean_square = [&](float by) {
     float s = 0.f;
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s = __builtin_fmaf(v[p].v[j], v[p].v[j], s);
+      for (int j = 0; j < 8; ++j) {
+        const float x = v[p].v[j] * by;
+        s = __builtin_fmaf(x, x, s);
+      }
     return sum(s) / n;
   };
   auto subtract = [&](float m) {
@@ -215,21 +219,50 @@ __global__ __launch_bounds__(BLOCK ? 64 * kNormMaxWaves : 256) void norm_kernel(
     float mean = 0.f;
     if (layer) {
       mean = mean_of();
+      // A sum past fp32 has a value of 2^112 or more. Either all are equal, or two are 2^88
+      // or more apart and the mean square is past fp32: zeros both times, NaN for what is
+      // not finite.
+      if (!(fabsf(mean) <= FLT_MAX)) {
+        mean = 0.f;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[p].v[j] -= v[p].v[j];
+      }
       subtract(mean);
     }
-    float square = mean_square();
+    float square = mean_square(1.f);
+    // Rows for which that is not it, a condition that all threads of a row share. Loops, so
+    // that they take no registers from the others.
     // The sum of a row rounds by up to some 90 half steps of its mean, which count among
-    // deviations that are small against it: beyond 64 times their root mean square (a
-    // condition of the row, the same in all its threads) they are taken from the fp32
-    // number next to the mean, which is the value itself in a row of equal ones, and then
-    // from their own mean. A loop, so that it takes no registers from the usual way.
-    if (mean * mean * 0x1p-12f > square) {
+    // deviations that are small against it: beyond 64 times their root mean square they
+    // are taken from the fp32 number next to the mean, which is the value itself in a row
+    // of equal ones, and then from their own mean.
+    // Squares whose sum is past fp32 are summed again of numbers times 2^-96: one is 2^56
+    // or more, so what that flushes to 0 does not count. A mean square that is past fp32
+    // itself stays infinite and makes zeros, of a deviation past fp32 too.
+    if (!(mean * mean * 0x1p-12f <= square && square <= FLT_MAX)) {
+      if (layer) {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            v[p].v[j] = fabsf(v[p].v[j]) > FLT_MAX ? copysignf(FLT_MAX, v[p].v[j]) : v[p].v[j];
+#pragma unroll 1
+        for (int round = 0; round < 2; ++round) {
+          float m = mean_of();
+          if (!(fabsf(m) <= FLT_MAX)) m = 0.f;  // so is the mean square then
+          subtract(round == 0 ? (mean + m) - mean : m);
+        }
+      }
+      float by = 1.f, back = 1.f;
 #pragma unroll 1
       for (int round = 0; round < 2; ++round) {
-        const float m = mean_of();
-        subtract(round == 0 ? (mean + m) - mean : m);
+        square = mean_square(by) * back * back;
+        if (square <= FLT_MAX) break;
+        by = 0x1p-96f;
+        back = 0x1p96f;
       }
-      square = mean_square();
     }
     const float r = 1.f / sqrtf(square + a.eps);
 #pragma unroll
@@ -323,20 +356,18 @@ __global__ __launch_bounds__(64) void norm_short_kernel(const NormArgs args) {
   auto bf16_at = [](const void* p, long long i) { return bf16_bits_to_f32(to_global(static_cast<const uint16_t*>(p))[i]); };
   float v[7];
   auto normalise = [&](const void* w, const void* b) {
-    double mean = 0.0;  // of at most 7 values: exact but for the quotient
-    float s = 0.f;
+    // In 64 bits: sums of at most 7 values, and of their squares, are exact there but for
+    // their last half steps, and none overflows.
+    double mean = 0.0, s = 0.0;
     if (a.kind == W4A16_NORM_LAYER) {
       for (int j = 0; j < 7; ++j) mean += j < N ? v[j] : 0.f;
       mean /= n;
     }
-    for (int j = 0; j < 7; ++j) {
-      v[j] = static_cast<float>(v[j] - mean);
-      s += j < N ? v[j] * v[j] : 0.f;
-    }
-    const float r = 1.f / sqrtf(s / n + a.eps);
+    for (int j = 0; j < 7; ++j) s += j < N ? (v[j] - mean) * (v[j] - mean) : 0.0;
+    const float r = 1.f / sqrtf(static_cast<float>(s / n) + a.eps);
     for (int j = 0; j < 7; ++j) {
       if (j >= N) continue;
-      v[j] *= r;
+      v[j] = static_cast<float>((v[j] - mean) * r);
       if (w) v[j] *= bf16_at(w, j) + (a.unit_offset ? 1.f : 0.f);
       if (b) v[j] += bf16_at(b, j);
     }
