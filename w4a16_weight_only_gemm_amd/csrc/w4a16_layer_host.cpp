@@ -68,9 +68,10 @@ int w4a16_norm(const w4a16_norm_args* a, int T, int N, hipStream_t stream) {
   if (!a->residual_out && !a->x && !a->xq) return W4A16_ERR_INVALID_ARG;
   if (T == 0) return W4A16_OK;
   if (N < 1 || N > W4A16_NORM_MAX_COLUMNS || (a->xq && N % 16 != 0)) return W4A16_ERR_UNSUPPORTED;
-  if (!aligned(a->y, 16) || !aligned(a->gate, 16) || !aligned(a->residual, 16) || !aligned(a->residual_out, 16) ||
-      !aligned(a->x, 16) || !aligned(a->xq, 16) || !aligned(a->sx, 4) || !aligned(a->weight, 2) ||
-      !aligned(a->bias, 2) || !aligned(a->post_weight, 2) || !aligned(a->post_bias, 2))
+  if (!aligned(a->y, 16) || !aligned(a->residual, 16) || !aligned(a->residual_out, 16) || !aligned(a->x, 16) ||
+      !aligned(a->xq, 16) || !aligned(a->sx, 4) || !aligned(a->weight, 2) || !aligned(a->bias, 2))
+    return W4A16_ERR_MISALIGNED;
+  if (a->y && (!aligned(a->gate, 16) || !aligned(a->post_weight, 2) || !aligned(a->post_bias, 2)))
     return W4A16_ERR_MISALIGNED;
   return status(w4a16_internal::launch_norm(*a, T, N, stream));
 }
