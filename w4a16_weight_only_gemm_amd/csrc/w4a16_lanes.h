@@ -1,5 +1,5 @@
 // w4a16_lanes.h -- a wave's lanes together: order-preserving keys, maxima and sums
-// over the wave, and the choice of a token's experts from them.
+// over the wave.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -7,8 +7,6 @@
 #include <cstdint>
 
 namespace w4a16_internal {
-
-constexpr int kRtMaxExperts = 1024;
 
 // Order-preserving bits: a < b as numbers iff key(a) < key(b) as unsigned.
 __device__ __forceinline__ uint32_t order_key(float f) {
@@ -78,40 +76,6 @@ __device__ __forceinline__ T wave_sum_of(T v) {
   v += dpp_of<0x141, 0xF>(v);
   v += dpp_of<0x140, 0xF>(v);
   return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
-}
-
-// The i-th expert of a lane. Choice by value takes consecutive ones, so that
-// groups are whole lanes; choice by logit takes every 64th, so that the order
-// of (i, lane) is that of the experts and equal keys need no second look.
-template <int P, bool WIDE>
-__device__ __forceinline__ int expert_of(int lane, int i) {
-  return WIDE ? lane * P + i : i * 64 + lane;
-}
-
-// The top_k largest keys (0: never), one after the other, the lowest expert of
-// equal ones first: lane j gets the j-th choice, -1 where nothing is left.
-template <int P, bool WIDE, typename Key>
-__device__ __forceinline__ int take(Key (&key)[P], int top_k, int lane) {
-  int id = -1;
-  for (int j = 0; j < top_k; ++j) {
-    Key best = key[0];
-    int bi = 0;
-#pragma unroll
-    for (int i = 1; i < P; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        bi = i;
-      }
-    const Key top = wave_max_of(best);
-    if (top == 0) break;
-    const uint32_t back = best == top ? kRtMaxExperts - expert_of<P, WIDE>(lane, bi) : 0;
-    const int e = kRtMaxExperts - static_cast<int>(wave_max_of(back));
-    if (lane == j) id = e;
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (expert_of<P, WIDE>(lane, i) == e) key[i] = 0;
-  }
-  return id;
 }
 
 }  // namespace w4a16_internal

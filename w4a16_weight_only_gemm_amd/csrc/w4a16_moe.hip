@@ -50,6 +50,7 @@ namespace {
 
 constexpr int kRtThreads = 1024;
 constexpr int kRtWaves = kRtThreads / 64;
+constexpr int kRtMaxExperts = 1024;
 // Tokens per workgroup (a wave takes one after the other), by the number of
 // tokens. A token takes a wave some 2 to 4 us of dependent steps, so few tokens
 // are spread over many workgroups; the second launch reads every chunk's
@@ -121,6 +122,40 @@ struct Token {
   float z[P];
   bool live[P];
 };
+
+// The i-th expert of a lane. Choice by value takes consecutive ones, so that
+// groups are whole lanes; choice by logit takes every 64th, so that the order
+// of (i, lane) is that of the experts and equal keys need no second look.
+template <int P, bool WIDE>
+__device__ __forceinline__ int expert_of(int lane, int i) {
+  return WIDE ? lane * P + i : i * 64 + lane;
+}
+
+// The top_k largest keys (0: never), one after the other, the lowest expert of
+// equal ones first: lane j gets the j-th choice, -1 where nothing is left.
+template <int P, bool WIDE, typename Key>
+__device__ __forceinline__ int take(Key (&key)[P], int top_k, int lane) {
+  int id = -1;
+  for (int j = 0; j < top_k; ++j) {
+    Key best = key[0];
+    int bi = 0;
+#pragma unroll
+    for (int i = 1; i < P; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        bi = i;
+      }
+    const Key top = wave_max_of(best);
+    if (top == 0) break;
+    const uint32_t back = best == top ? kRtMaxExperts - expert_of<P, WIDE>(lane, bi) : 0;
+    const int e = kRtMaxExperts - static_cast<int>(wave_max_of(back));
+    if (lane == j) id = e;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (expert_of<P, WIDE>(lane, i) == e) key[i] = 0;
+  }
+  return id;
+}
 
 // The same from 32-bit keys whose low bits (P - 1, a mask) give way to P - 1 -
 // i, so that a key names its expert within the lane: a lane's keys are sorted

@@ -493,8 +493,9 @@ struct MlPlan {
   float chosen[kMlTokens][kMlMaxK];
   int active;  // experts with tokens
   // behind it, `most` entries each:
-  //   float weight[most][16], short expert[most], short tokens[most] (a bit each),
-  //   uint8 place[most][16]; then short index[E]
+  //   float weight[most][16], uint8 place[most][16], short expert[most], short
+  //   mask[most] (a bit per token); then uint32 tokens[E]: while the plan is made an
+  //   expert's bits, then its entry
 };
 __host__ __device__ constexpr size_t ml_plan_bytes(int most, int E) {
   return (sizeof(MlPlan) + 15) / 16 * 16 + static_cast<size_t>(most) * (64 + 2 + 2 + 16) +
@@ -504,7 +505,7 @@ __host__ __device__ constexpr size_t ml_plan_bytes(int most, int E) {
 struct MlTables {
   MlPlan* plan;
   float* weight;     // [most][16]
-  uint32_t* tokens;  // [E] while the plan is made: a bit per token
+  uint32_t* tokens;  // [E] while the plan is made: a bit per token, then the entry
   uint8_t* place;    // [most][16]
   short* expert;     // [most]
   short* mask;       // [most]
