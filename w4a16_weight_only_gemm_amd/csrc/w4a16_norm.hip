@@ -210,7 +210,7 @@ __global__ __launch_bounds__(BLOCK ? 64 * kNormMaxWaves : 256) void norm_kernel(
     for (int p = 0; p < P; ++p) {
       int left = span[p].left;
       // compared here: masks of all columns, made once for every use, fill the registers
-      asm volatile("" : "+v"(left));
+      asm volatile("" : "+v"(left) : :);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[p].v[j] = (TAIL ? j < left : left > 0) ? v[p].v[j] - m : 0.f;
     }
