@@ -109,9 +109,10 @@ typedef struct w4a16_norm_args {
  * With xq and sx instead of x: a = max |v|, sx[t] = a / 127, codes v * (127 / a)
  * rounded to the nearest integer (ties to even) in -127 .. 127; 0 and sx 0 for a
  * row of zeros. Inputs of rows that are written as codes must be finite.
- * The mean of squares of a layer norm is taken of the deviations themselves. A
- * mean of squares past fp32 is infinite, and its row comes out as zeros (and
- * biases), as the formula in fp32 has it.
+ * The mean of squares of a layer norm is taken of the deviations themselves, which
+ * are 0 in a row of equal values, whatever they are. A mean of squares past fp32 is
+ * infinite, and its row comes out as zeros (and biases), as the formula in fp32
+ * has it; a sum on the way to a mean inside fp32 may be past it.
  * Supported: T >= 0, 1 <= N <= W4A16_NORM_MAX_COLUMNS, for codes N % 16 == 0; a
  * grid of fewer than 2^32 threads (else W4A16_ERR_UNSUPPORTED). y, gate, residual,
  * residual_out, x and xq 16-byte aligned, the vectors 2-byte, sx 4-byte. Outputs
@@ -152,7 +153,7 @@ size_t w4a16_moe_layer_workspace_bytes(int T, int experts, int top_k, int hidden
  *   ids, weights: the choice that w4a16_moe_route defines, from these logits;
  *     a token whose `live` is 0 is routed nowhere (ids -1, weights 0)
  *   h[t][j] = silu(x[t] . gate half) * (x[t] . up half) of expert ids[t][j],
- *     held to 16 bits (two bf16)
+ *     held to 16 bits (two bf16); past what bf16 holds the token's row is NaN
  *   out[t] = base[t] + sum_j weights[t][j] * (h[t][j] . down of expert ids[t][j])
  * with fp32 products and sums and one rounding to bf16 at the end. A result
  * does not depend on timing: the same call gives the same bits.

@@ -15,7 +15,7 @@
 //  * gate_up_kernel: a wave owns a range of K and holds its tokens' activations of that
 //    range in registers, while the weights of one (expert, 16 gate and 16 up columns)
 //    after the other stream by, a whole task ahead. The waves' sums meet in LDS, where
-//    SwiGLU is formed. 16 tokens of 128 experts, 5120 x 1024: 6.7 TB/s while it streams.
+//    SwiGLU is formed. 13 tokens of 128 experts, 5120 x 1024: 393 MB in 60 to 64 us.
 //    SwiGLU's values are stored as two bf16 (down_kernel says why).
 //  * down_kernel: the active experts' k ranges laid end to end are one long sum for every
 //    16 columns of the output, each expert's part weighted by its tokens' weights on the
@@ -23,11 +23,18 @@
 //    added by the last workgroup to finish one, in their order, so results do not depend
 //    on timing.
 // Bound by HBM from a few tokens on (16 tokens of 128 experts, 5120 x 1024: 118 to 127 us,
-// 4.7 to 5.0 TB/s over all of it); at one token (28 us) by three launches' ramps and by the
-// chain logits, choice, first weights. Gate, up and down in one launch, whose workgroups
-// wait for the inner rows with down's first weights on their way, took 30 us there and 123
-// at 16 tokens, when separate launches took 27 and 122: the rows' way through memory and
-// the polls behind the weights cost more than a launch.
+// 4.7 to 5.0 TB/s over all of it); at few (one: 28 us) by three launches' ramps, by the chain
+// logits, choice, first weights, and by down_kernel's end, where the last workgroup's loads
+// of the parts wait for one another (2 values a thread, a load for each part of one).
+// Up to 16 tokens: one row block of the matrix instruction. There it is ahead of the router's
+// product, w4a16_moe_route, w4a16_gemm_experts twice and w4a16_moe_combine in one graph (us,
+// this / those, at 1, 4, 16 tokens): 8 of 128 experts of 5120 x 1024 30 / 45, 60 / 81, 132 /
+// 153; 8 of 256 of 5120 x 512 in groups 30 / 42, 48 / 62, 91 / 110; 4 of 32 of 2048 x 768 21 /
+// 31, 28 / 35, 41 / 46.
+// Gate, up and down in one launch, whose workgroups wait for the inner rows with down's
+// first weights on their way, took 30 us at one token and 123 at 16, when separate launches
+// took 27 and 122: the rows' way through memory and the polls behind the weights cost more
+// than a launch.
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
@@ -1085,6 +1092,11 @@ hipError_t launch_moe_layer_g(const MlArgs& a, bool half, hipStream_t stream) {
   }
   constexpr int kPer = U::K / 128;
   const int held = ((a.H / GS + U::G - 1) / U::G + kMlWaves - 1) / kMlWaves * kPer;  // 128s of K per wave
+  // The next larger form that is built; loads of units that a wave has not are not made. us
+  // of the whole layer, 8 of 64 experts of width 1024, at groups of 128 and 64: five units
+  // by their own form and by six, 1 token 28.1 / 28.5 and 31.6 / 33.2, 16 tokens 102 / 105
+  // and 115 / 119; three by four and by a form of their own 24.0 / 23.9 and 26.5 / 25.4,
+  // 67.6 / 66.1 and 80.4 / 75.4; seven by eight and by their own 33.0 / 32.4, 134 / 132.
   if (held <= 2)
     e = launch_gate_up<GS, 2 / kPer>(a, stream);
   else if (held <= 4)

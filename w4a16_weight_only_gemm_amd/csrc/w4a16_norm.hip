@@ -9,8 +9,10 @@
 // two more where the mean's rounding counts among them), and r and v are rounded
 // once, on their way out. A row belongs to 16, 32 or 64 lanes of a wave (DPP sums, no
 // LDS) or to the waves of a workgroup (one barrier a sum).
-// What bounds it: HBM for many rows; for few, the launch and the chain of a load,
-// the sums and a store.
+// What bounds it: HBM for many long rows (4095 of 5120, fp32 residual: 52.4 us, 252 MB);
+// otherwise the launch and a chain of loads, sums and a store: every operand's pieces are
+// asked for behind its own condition and waited for one after the other, 14 such waits in
+// the form of 2048 rows of 2741 with gate and layer norms on both sides (17 us).
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
@@ -150,7 +152,8 @@ struct RowJoin {
 // are contiguous. TAIL: N is no multiple of 8 (and at least 8).
 // Only y is asked for in front of the first sum. Asking for everything there costs
 // registers, and waves that would hide the waits more cheaply: 2048 rows of 2741, layer
-// norms on both sides and a gate 22.1 against 17.3 us.
+// norms on both sides and a gate 22.1 against 17.3 us (two pieces a thread; one piece,
+// which needs 33 to 39 registers, and loads together within a step were not tried).
 template <int P, int L, bool BLOCK, bool TAIL>
 __global__ __launch_bounds__(BLOCK ? 64 * kNormMaxWaves : 256) void norm_kernel(const NormArgs args) {
   const w4a16_norm_args& a = args.a;
@@ -432,6 +435,8 @@ hipError_t launch_norm(const w4a16_norm_args& a, int T, int N, hipStream_t strea
   // (1000 rows of 17408: 35.5 us with three, 46.3 with four)
   if (pieces <= 3 * 64 * kNormMaxWaves) return launch_norm_block<3>(args, pieces, stream);
   if (pieces <= 4 * 64 * kNormMaxWaves) return launch_norm_block<4>(args, pieces, stream);
+  // rows past 32768, which this form's 64 values fill the registers with: 7 of a thread's 128
+  // lie in scratch memory, 33 with odd lengths (500 rows of 65536: 72 us, of 65535: 104)
   return launch_norm_block<8>(args, pieces, stream);
 }
 
